@@ -16,7 +16,7 @@ from . import _abi
 from ._abi import (  # noqa: F401
     F32, BF16, E4M3, SCORE_CUMULATIVE, SCORE_EMA, SCORE_TOKEN_SUM, SCORE_TOVA, KERNEL_AUTO, KERNEL_GENERAL,
     KERNEL_TENSOR,
-    MODE_NONE, MODE_WINDOW, MODE_H2O, SELECT_PROTECT, SELECT_APPLY, Config, Layout,
+    MODE_NONE, MODE_WINDOW, MODE_H2O, SELECT_PROTECT, SELECT_APPLY, Config, Layout, PagedConfig,
 )
 from ._abi import (  # noqa: F401
     STATE_K_PAGES, STATE_V_PAGES, STATE_K_SCALES, STATE_V_SCALES, STATE_POSITIONS, STATE_NEXT_POSITION,
@@ -356,3 +356,6 @@ class KVCache:
 
     def last_error(self):
         return lib().kvs_last_error(self._ctx).decode()
+
+
+from .paged import PagedCache, PagedPlan, paged_config_init, validate_paged_config, paged_workspace_bytes  # noqa: E402,F401

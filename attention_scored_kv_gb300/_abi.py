@@ -54,6 +54,12 @@ class Seqs(ctypes.Structure):
                 ("d_ids", ctypes.c_void_p)]
 
 
+class PagedConfig(ctypes.Structure):
+    _fields_ = [("num_layers", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("block_tokens", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("kernel", ctypes.c_int32), ("reserved", ctypes.c_int32 * 8)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _S = Seqs
@@ -86,6 +92,21 @@ _SIGS = {
     "kvs_status_string": (ctypes.c_char_p, [_I]),
     "kvs_abi_version": (_I, []),
     "kvs_build_info": (ctypes.c_uint32, []),
+    "kvs_paged_config_init": (None, [ctypes.POINTER(PagedConfig)]),
+    "kvs_paged_validate_config": (_I, [ctypes.POINTER(PagedConfig), ctypes.c_char_p, ctypes.c_size_t]),
+    "kvs_paged_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PagedConfig)]),
+    "kvs_paged_create": (_I, [ctypes.POINTER(PagedConfig), _P, ctypes.c_size_t, _P, ctypes.POINTER(_P)]),
+    "kvs_paged_destroy": (_I, [_P]),
+    "kvs_paged_plan": (_I, [_P, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
+    "kvs_paged_slot_map": (_I, [_P, _I, _P, _P, _P, _I, _P, _P, _P, _I, _P]),
+    "kvs_paged_release": (_I, [_P, _I, _P, _P, _I, _P, _I, _P, _P]),
+    "kvs_paged_append": (_I, [_P, _I, _I, _P, _P, _P, _P]),
+    "kvs_paged_gather": (_I, [_P, _I, _I, _P, _P, _P, _P]),
+    "kvs_paged_attend_scratch_bytes": (ctypes.c_size_t, [_P, _I, _I, _I, _I, _I]),
+    "kvs_paged_attend": (_I, [_P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kvs_paged_get_status": (_I, [_P, _P]),
+    "kvs_paged_clear_error": (_I, [_P, _P]),
+    "kvs_paged_last_error": (ctypes.c_char_p, [_P]),
 }
 
 _lib = None

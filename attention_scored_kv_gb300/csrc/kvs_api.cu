@@ -5,7 +5,6 @@
 // checked and sized without reading device memory.  The device holds the truth; a
 // replayed CUDA graph advances the device state but not these shadows.
 #include <cuda.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <cstdlib>
@@ -18,6 +17,7 @@
 #include <vector>
 
 #include "kvs_internal.cuh"
+#include "trace.cuh"
 
 namespace kvs {
 bool tc_supported(int Hq, int Hkv, int D, int kv_dtype, int in_dtype, int window, int mode);
@@ -38,29 +38,6 @@ using namespace kvs;
 namespace {
 
 constexpr int32_t kDefaultSpin = 5000000;   // ~0.5 s of 100 ns polls
-
-// NVTX ranges around every ABI call, for profiler timelines (Nsight Systems, ncu's
-// range filters): on when the environment variable KVS_NVTX is set to anything but
-// "0" when the library is first used.  Without an attached tool the calls do nothing.
-bool tracing_on() {
-  static const bool on = [] {
-    const char* v = std::getenv("KVS_NVTX");
-    return v && *v && std::strcmp(v, "0") != 0;
-  }();
-  return on;
-}
-
-struct Trace {
-  explicit Trace(const char* name) : on(tracing_on()) {
-    if (on) nvtxRangePushA(name);
-  }
-  ~Trace() {
-    if (on) nvtxRangePop();
-  }
-  Trace(const Trace&) = delete;
-  Trace& operator=(const Trace&) = delete;
-  bool on;
-};
 
 struct Plan {
   int mode = 0, pages_per_seq = 0, num_pages = 0, max_blocks = 0, res_blocks_per_seq = 0;

@@ -1,0 +1,117 @@
+// The paged E4M3 cache: shared declarations of its translation units.
+//
+// Workspace (256-byte aligned regions, zeroed at creation), per layer:
+//   K codes  [num_pages][Hkv][2][D/16][8][16]   token t, dimension d at
+//            [t / 8][d / 16][t % 8][d % 16]
+//   V codes  [num_pages][Hkv][D][16]            token innermost
+//   scales   [num_pages][Hkv] float2            (K scale, V scale), powers of two
+// and one error word.  Both code layouts are made of 128-byte "core matrices" (8 rows of
+// 16 bytes), which is what the tensor core's unswizzled K-major operands are made of: K
+// rows are tokens with the contraction over d, V rows are dimensions with the
+// contraction over tokens.  A page is one contiguous 16 * D bytes in each, so a plain bulk copy of it
+// lands in shared memory as operand rows, and neither K nor V needs to be transposed,
+// swizzled or (as the matrix instruction takes E4M3 operands) converted.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "kvs_internal.cuh"
+
+namespace kvs {
+
+constexpr int kScaleMinExp = -100;       // exponents a page scale can have
+constexpr int kScaleMaxExp = 119;
+constexpr int kMaxGroup = 64;            // query heads per KV head at most
+
+struct PagedDev {
+  int32_t L, Hq, Hkv, G, D, num_pages, in_dtype;
+  uint8_t* k; uint8_t* v; size_t layer_bytes;      // num_pages * Hkv * 16 * D
+  float2* scales; size_t layer_scales;             // num_pages * Hkv
+  int32_t* err;
+};
+
+// One attend call, as the kernels see it.
+struct PagedAttend {
+  PagedDev d;
+  int32_t layer, n_reqs, table_stride, total_q, max_q_len, window;
+  const int32_t* table; const int32_t* kv_len; const int32_t* row_start;   // row_start may be null
+  const void* q; void* out;
+  float* mass;             // [n_reqs][table_stride] or null
+  // scratch
+  float* part_o;           // partial output rows
+  float2* part_ml;         // their (reference maximum in log2 units, sum)
+  float* blk;              // [n_reqs][table_stride][Hq] log2 of the blocks' weight sums (mass only)
+  float* lse;              // [n_reqs][Hq] log2 of the rows' sums (mass only)
+  int32_t splits;          // general kernel: parts of a row's range
+};
+
+// How a call runs: a pure function of host-known sizes, so that the scratch size and the
+// launch agree.
+struct PagedAttendPlan {
+  bool tensor;
+  int splits;              // general kernel
+  int rows;                // tensor decode kernel: query rows of a unit (0 = not launched)
+  bool prompt;             // tensor prompt kernel launched
+  int grid;                // tensor decode kernel
+  size_t part_o, part_ml, blk, lse, total;   // scratch offsets
+};
+
+__host__ __device__ inline size_t k_code(int D, int t, int d) {
+  return (size_t)(t >> 3) * 8 * D + (size_t)(d >> 4) * 128 + (t & 7) * 16 + (d & 15);
+}
+
+__device__ __forceinline__ void paged_error(const PagedDev& d, int32_t bits) { atomicOr(d.err, bits); }
+
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+
+// Exponent of the smallest power of two s with absmax <= 448 * s (448 = 1.75 * 2^8):
+// from the bits, so that it is exact; clamped to the exponents a scale can have.
+__device__ __forceinline__ int scale_exp(float absmax) {
+  const int bits = __float_as_int(absmax);
+  const int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+  return max(kScaleMinExp, min(kScaleMaxExp, e));
+}
+
+// Two E4M3 codes as floats (exact).
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes16) {
+  uint32_t h;
+  const uint16_t c = (uint16_t)codes16;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Codes of (lo, hi), round to nearest even, saturating.
+__device__ __forceinline__ uint32_t float2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Request of packed row t: the last r with row_start[r] <= t.
+__device__ __forceinline__ int request_of(const int32_t* row_start, int n, int t) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(row_start + mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+cudaError_t launch_paged_plan(const PagedDev& d, int n, const int32_t* ctx, const int32_t* add, int32_t* table,
+                              int stride, const int32_t* free_pages, int free_capacity, const int32_t* count_in,
+                              int32_t* count_out, int32_t* row_start, int32_t* kv_len, int32_t* slots,
+                              int32_t* positions, int capacity, int32_t* denied, int sms, cudaStream_t st);
+cudaError_t launch_paged_slot_map(const PagedDev& d, int n, const int32_t* first, const int32_t* len,
+                                  const int32_t* table, int stride, int32_t* row_start, int32_t* slots,
+                                  int32_t* positions, int capacity, int sms, cudaStream_t st);
+cudaError_t launch_paged_release(const PagedDev& d, int n, const int32_t* kv_len, int32_t* table, int stride,
+                                 int32_t* free_pages, int free_capacity, int32_t* free_count, cudaStream_t st);
+cudaError_t launch_paged_append(const PagedDev& d, int layer, int n_rows, const int32_t* slots, const void* k,
+                                const void* v, cudaStream_t st);
+cudaError_t launch_paged_gather(const PagedDev& d, int layer, int n_rows, const int32_t* slots, void* k, void* v,
+                                cudaStream_t st);
+cudaError_t launch_paged_general(const PagedAttend& a, cudaStream_t st);
+cudaError_t launch_paged_mass(const PagedAttend& a, cudaStream_t st);
+
+}  // namespace kvs

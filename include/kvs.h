@@ -469,6 +469,170 @@ KVS_API int32_t kvs_abi_version(void);
 /* How this library was built and what it emits (KVS_BUILD_* bits). */
 KVS_API uint32_t kvs_build_info(void);
 
+/* ------------------------------------------------------------------ the paged cache
+ *
+ * A second cache beside kvs_ctx, for serving batches whose requests come, grow and go:
+ * every length, block table and slot is device data, so no call needs to know a length
+ * on the host and a captured graph can be replayed while the batch changes.  It holds K
+ * and V as E4M3 codes in pages of 16 tokens, with one scale per page and KV head for
+ * each of K and V (kvs_ctx keeps one scale per position for all KV heads).
+ *
+ *   per step:            kvs_paged_plan     block tables, slots, positions, lengths
+ *   for every layer:     kvs_paged_append   store the new tokens' K and V
+ *                        kvs_paged_attend   attend the new tokens' queries
+ *   request finished:    kvs_paged_release  its pages go back to the free stack
+ *
+ * Scales are powers of two: for a page and KV head the smallest 2^e, -100 <= e <= 119,
+ * with every |x| of its tokens <= 448 * 2^e (448 is the largest E4M3 value; what passes
+ * 448 * 2^119 saturates).  A power of
+ * two costs a floating-point code no precision, and makes a value's product with its
+ * scale exact, so a page whose scale grows is re-rounded only where a value falls under
+ * the smallest normal code.
+ *
+ * Tables and lengths are the caller's device arrays.  A request r is row r of them:
+ *   block_table  [n_reqs][table_stride] int32, entry b the page of positions
+ *                16 b .. 16 b + 15; entries past a request's length are not read
+ *   slot         page * 16 + position % 16; negative = none
+ *   rows         new tokens are packed by request: rows row_start[r] .. row_start[r+1]-1
+ * A page in a table or slot that is not in [0, num_pages) is never followed: the token or
+ * block is left out and kvs_paged_get_status() reports KVS_ERR_STATE.
+ *
+ * The conventions above hold (status codes, streams, caller-owned workspace).  A call
+ * runs on the device that was current at kvs_paged_create(), whatever device is current
+ * now; the stream must belong to that device.  Calls on one kvs_paged from several host
+ * threads need a lock of the caller's (the message of kvs_paged_last_error is shared).
+ * Device work on several streams may overlap as long as no page is appended while
+ * another call reads or appends it. */
+typedef struct kvs_paged kvs_paged;
+
+typedef struct {
+  int32_t num_layers;        /* >= 1 */
+  int32_t num_q_heads;       /* Hq, a multiple of num_kv_heads */
+  int32_t num_kv_heads;      /* Hkv, at most 1024; Hq / Hkv at most 64 */
+  int32_t head_dim;          /* D in {16, 32, 64, 128} */
+  int32_t num_pages;         /* pages of the pool, 1 .. 2^27 - 1 (every layer has as many) */
+  int32_t block_tokens;      /* 16 (the only value supported) */
+  int32_t in_dtype;          /* dtype of K, V, Q and of the outputs: KVS_F32 or KVS_BF16 */
+  int32_t kernel;            /* a kvs_kernel: AUTO takes the tensor-core attend for bf16 and
+                                head_dim 64 or 128, GENERAL never takes it, TENSOR refuses
+                                other configs */
+  int32_t reserved[8];       /* must be 0 */
+} kvs_paged_config;
+
+/* Fill *cfg with defaults (block 16, bf16, AUTO; the sizes 0). */
+KVS_API void kvs_paged_config_init(kvs_paged_config* cfg);
+
+/* As kvs_validate_config, kvs_workspace_bytes, kvs_create and kvs_destroy.  Per layer the
+ * workspace holds codes of 2 * num_pages * Hkv * 16 * D bytes and 8 * num_pages * Hkv
+ * bytes of scales; their layout inside is the library's (kvs_paged_gather reads values
+ * back).  kvs_paged_create zeroes it. */
+KVS_API kvs_status kvs_paged_validate_config(const kvs_paged_config* cfg, char* msg, size_t msg_len);
+KVS_API size_t kvs_paged_workspace_bytes(const kvs_paged_config* cfg);
+KVS_API kvs_status kvs_paged_create(const kvs_paged_config* cfg, void* d_workspace, size_t workspace_bytes,
+                                    kvs_stream_t stream, kvs_paged** out);
+KVS_API kvs_status kvs_paged_destroy(kvs_paged* pc);
+
+/* Block tables, slots and lengths of one step, from the requests' lengths.  No page
+ * counterpart: it is the bookkeeping that the paged blocks of "Per-Head Attention as a
+ * Scoring Signal" imply when requests join and leave a batch.
+ *   d_ctx_len, d_new_len   [n_reqs] int32 in: tokens cached, tokens to add (either may be 0)
+ *   d_block_table          in/out: blocks ceil(ctx/16) .. ceil((ctx+new)/16)-1 of each request
+ *                          get pages; other entries are left as they were
+ *   d_free_pages           [free_capacity] int32 in: the free stack, its top at
+ *                          d_free_count_in[0] - 1
+ *   d_free_count_out       [1]: the count left (may be d_free_count_in)
+ *   d_row_start            [n_reqs + 1] out: packed rows, the exclusive sums of new_len
+ *   d_kv_len               [n_reqs] out: ctx + new (may be d_ctx_len)
+ *   d_slots, d_positions_opt  [row_capacity] out, the latter may be NULL: slot and absolute
+ *                          position of each row; rows past the last get slot -1, position 0
+ *   d_denied_opt           [1] out or NULL: requests denied
+ * The j-th page taken (requests in order, then blocks) is free_pages[count - 1 - j].  A
+ * request is denied when its tokens pass table_stride * 16 or the pages that it and the
+ * requests before it want are more than the stack holds (a request that wants no page is
+ * not denied for the latter).  A denied request takes no page, keeps kv_len = ctx and has
+ * slot -1 in all its rows, so that a batch that was packed before the call still lines up.
+ * A negative length counts as 0 and rows beyond row_capacity are dropped; these and a
+ * denied request are reported by kvs_paged_get_status (KVS_ERR_STATE, KVS_ERR_CAPACITY).
+ * Outputs must not overlap inputs or one another except where said.  One launch. */
+KVS_API kvs_status kvs_paged_plan(kvs_paged* pc, int32_t n_reqs, const int32_t* d_ctx_len, const int32_t* d_new_len,
+                                  int32_t* d_block_table, int32_t table_stride, const int32_t* d_free_pages,
+                                  int32_t free_capacity, const int32_t* d_free_count_in, int32_t* d_free_count_out,
+                                  int32_t* d_row_start, int32_t* d_kv_len, int32_t* d_slots,
+                                  int32_t* d_positions_opt, int32_t row_capacity, int32_t* d_denied_opt,
+                                  kvs_stream_t stream);
+
+/* Slots (and positions) of positions first .. first + len - 1 of each request, packed, from
+ * block tables that are already filled: the slot map of kvs_paged_plan without taking
+ * pages, for reading a context back.  d_first_opt: [n_reqs] int32, NULL = all 0.  Arguments
+ * and limits as there; a position past table_stride * 16 gets slot -1 and is reported as
+ * KVS_ERR_CAPACITY. */
+KVS_API kvs_status kvs_paged_slot_map(kvs_paged* pc, int32_t n_reqs, const int32_t* d_first_opt, const int32_t* d_len,
+                                      const int32_t* d_block_table, int32_t table_stride, int32_t* d_row_start,
+                                      int32_t* d_slots, int32_t* d_positions_opt, int32_t row_capacity,
+                                      kvs_stream_t stream);
+
+/* Return the pages of finished requests (blocks 0 .. ceil(kv_len/16)-1 of each) to the free
+ * stack and set their table entries to -1.  The stack is left as if the pages had never
+ * been taken by a kvs_paged_plan that took them in this order.  Pages that do not fit in
+ * free_capacity are dropped (KVS_ERR_CAPACITY by kvs_paged_get_status), entries that are
+ * not a page are skipped over as a dropped -1 (KVS_ERR_STATE).  A page shared by several
+ * requests must be released once only.  d_free_count: [1] in/out.  One launch. */
+KVS_API kvs_status kvs_paged_release(kvs_paged* pc, int32_t n_reqs, const int32_t* d_kv_len, int32_t* d_block_table,
+                                     int32_t table_stride, int32_t* d_free_pages, int32_t free_capacity,
+                                     int32_t* d_free_count, kvs_stream_t stream);
+
+/* Store n_rows tokens of one layer (Flash-MoE "Context Optimization", FP8 KV Cache > How It
+ * Works, Encoding, with the scale kept per block and head instead of per position).
+ * d_k, d_v: [n_rows][Hkv][D] in in_dtype, 16-byte aligned; d_slots: [n_rows] int32.  Rows
+ * whose slot is negative are skipped.  Rows of one page must be neighbours and its slots
+ * distinct, as kvs_paged_plan makes them (else that page's contents are unspecified).
+ * A run that contains the page's first slot starts the page: its old scale and codes are
+ * dropped and the slots without a row become zero.  Otherwise the page's scale grows to
+ * what the run needs, if it does, and the other slots are re-rounded to it.
+ * Codes are round-to-nearest-even of x / scale.  An infinity saturates (it has no part in
+ * the scale); a NaN is stored as 0 and reported as KVS_ERR_STATE, so that a cache holds
+ * finite values only.  n_rows 0 is allowed. */
+KVS_API kvs_status kvs_paged_append(kvs_paged* pc, int32_t layer, int32_t n_rows, const int32_t* d_slots,
+                                    const void* d_k, const void* d_v, kvs_stream_t stream);
+
+/* The inverse: d_k, d_v [n_rows][Hkv][D] in in_dtype receive code * scale of the tokens at
+ * d_slots (exact in either type), zero where the slot is negative.  Slots in any order;
+ * a slot may be read any number of times.  n_rows 0 is allowed. */
+KVS_API kvs_status kvs_paged_gather(kvs_paged* pc, int32_t layer, int32_t n_rows, const int32_t* d_slots, void* d_k,
+                                    void* d_v, kvs_stream_t stream);
+
+/* Attention of packed ragged queries over the paged cache ("Context views at marginal
+ * cost", Fact 3; Flash-MoE "Context Optimization", FP8 KV Cache > How It Works, Decoding).
+ * d_q, d_out: [total_q][Hq][D] in in_dtype, 16-byte aligned.  Rows row_start[r] ..
+ * row_start[r+1]-1 are the last tokens of request r, oldest first: the i-th of n is at
+ * position kv_len[r] - n + i and sees the positions up to its own, with window > 0 only the
+ * last `window` of them.  Logits q.k/sqrt(D); softmax per head; query head h reads KV head
+ * h / (Hq / Hkv).  A row that sees nothing gets zeros.  Rows past row_start[n_reqs] are left
+ * as they were.  d_row_start NULL: one row per request (total_q must be n_reqs).
+ * max_q_len: at least the most rows any request has (1 when d_row_start is NULL); rows past
+ * it, or past total_q, are left as they were and reported as KVS_ERR_CAPACITY.  kv_len is
+ * clamped to [0, table_stride * 16].
+ * d_block_mass_opt (max_q_len 1 only): [n_reqs][table_stride] float32; entry b of request r
+ * receives the maximum over query heads of the head's weight in block b ("Per-Head
+ * Attention as a Scoring Signal", Fix: score per head, place per block), for the blocks
+ * that the row sees a part of; other entries are left as they were.
+ * d_scratch: device memory of kvs_paged_attend_scratch_bytes(), 256-byte aligned, whose
+ * contents before and after mean nothing; calls that may overlap need scratch of their
+ * own.  Probabilities are rounded to 16 bits or finer before their product with V (bf16
+ * in_dtype); sums and softmax statistics are float32. */
+KVS_API size_t kvs_paged_attend_scratch_bytes(const kvs_paged* pc, int32_t n_reqs, int32_t table_stride,
+                                              int32_t total_q, int32_t max_q_len, int32_t block_mass);
+KVS_API kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const int32_t* d_block_table,
+                                    int32_t table_stride, const int32_t* d_kv_len, const int32_t* d_row_start,
+                                    int32_t total_q, int32_t max_q_len, int32_t window, const void* d_q, void* d_out,
+                                    float* d_block_mass_opt, void* d_scratch, size_t scratch_bytes,
+                                    kvs_stream_t stream);
+
+/* As kvs_get_status, kvs_clear_error and kvs_last_error. */
+KVS_API kvs_status kvs_paged_get_status(kvs_paged* pc, kvs_stream_t stream);
+KVS_API kvs_status kvs_paged_clear_error(kvs_paged* pc, kvs_stream_t stream);
+KVS_API const char* kvs_paged_last_error(const kvs_paged* pc);
+
 #ifdef __cplusplus
 }
 #endif
