@@ -98,6 +98,15 @@ __device__ __forceinline__ int request_of(const int32_t* row_start, int n, int t
   return lo;
 }
 
+// Reports device row counts that pass what the host was told (one block of `threads`).
+__device__ __forceinline__ void report_rows(const PagedAttend& a, int threads) {
+  if (!a.row_start) return;
+  for (int r = threadIdx.x; r < a.n_reqs; r += threads) {
+    const int lo = __ldg(a.row_start + r), hi = __ldg(a.row_start + r + 1);
+    if (lo < 0 || hi < lo || hi - lo > a.max_q_len || hi > a.total_q) paged_error(a.d, kErrCapacity);
+  }
+}
+
 cudaError_t launch_paged_plan(const PagedDev& d, int n, const int32_t* ctx, const int32_t* add, int32_t* table,
                               int stride, const int32_t* free_pages, int free_capacity, const int32_t* count_in,
                               int32_t* count_out, int32_t* row_start, int32_t* kv_len, int32_t* slots,
@@ -111,6 +120,8 @@ cudaError_t launch_paged_append(const PagedDev& d, int layer, int n_rows, const 
                                 const void* v, cudaStream_t st);
 cudaError_t launch_paged_gather(const PagedDev& d, int layer, int n_rows, const int32_t* slots, void* k, void* v,
                                 cudaStream_t st);
+int paged_decode_ctas_per_sm();
+cudaError_t launch_paged_decode(const PagedAttend& a, int rows, int grid, cudaStream_t st);
 cudaError_t launch_paged_general(const PagedAttend& a, cudaStream_t st);
 cudaError_t launch_paged_mass(const PagedAttend& a, cudaStream_t st);
 

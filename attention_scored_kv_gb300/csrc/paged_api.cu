@@ -63,7 +63,7 @@ struct OnDevice {
 };
 
 bool tensor_shape(const kvs_paged_config* c) {
-  return false;
+  return c->in_dtype == KVS_BF16 && (c->head_dim == 64 || c->head_dim == 128);
 }
 
 kvs_status check_config(const kvs_paged_config* c, char* msg, size_t n) {
@@ -118,13 +118,22 @@ PagedAttendPlan plan_attend(const kvs_paged* pc, int n_reqs, int stride, int tot
   PagedAttendPlan p = {};
   const PagedDev& d = pc->dev;
   size_t recs = 0;
-  // a part per idle CTA, four CTAs to an SM, no part under a page a warp
-  const long long units = (long long)total_q * d.Hkv;
-  long long want = units > 0 ? (long long)pc->sms * 4 / units : 1;
-  if (want > 64) want = 64;
-  if (want > stride / 4) want = stride / 4;
-  p.splits = want < 1 ? 1 : (int)want;
-  if (p.splits > 1) recs = (size_t)total_q * d.Hq * p.splits;
+  const long long need = (long long)max_q_len * d.G;       // query rows of a unit
+  p.tensor = pc->tensor && need <= 32;
+  if (p.tensor) {
+    p.rows = need <= 8 ? 8 : need <= 16 ? 16 : 32;
+    p.grid = paged_decode_ctas_per_sm() * pc->sms;
+    p.splits = 1;
+    recs = (size_t)2 * p.grid * p.rows;                    // a CTA leaves at most two partials
+  } else {
+    // a part per idle CTA, four CTAs to an SM, no part under a page a warp
+    const long long units = (long long)total_q * d.Hkv;
+    long long want = units > 0 ? (long long)pc->sms * 4 / units : 1;
+    if (want > 64) want = 64;
+    if (want > stride / 4) want = stride / 4;
+    p.splits = want < 1 ? 1 : (int)want;
+    if (p.splits > 1) recs = (size_t)total_q * d.Hq * p.splits;
+  }
   p.part_o = 0;
   p.part_ml = p.part_o + up(recs * d.D * sizeof(float));
   p.blk = p.part_ml + up(recs * sizeof(float2));
@@ -350,7 +359,7 @@ kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const 
   a.lse = d_block_mass_opt ? reinterpret_cast<float*>(s + p.lse) : nullptr;
   a.splits = p.splits;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_paged_general(a, cs);
+  cudaError_t e = p.tensor ? launch_paged_decode(a, p.rows, p.grid, cs) : launch_paged_general(a, cs);
   if (e == cudaSuccess && a.mass) e = launch_paged_mass(a, cs);
   return cuda_ok(pc, e, "attend");
 }

@@ -1,0 +1,650 @@
+// Tensor-core attention over the paged cache for few query rows: single tokens and the
+// few tokens of a speculative step (bf16 queries, head_dim 64 or 128).
+//
+// For a unit (request, KV head) with R query rows (tokens x heads of the group) and a
+// tile of 128 cached tokens j:
+//   S^T = K Q^T        [128 tokens x rows]   E4M3 x E4M3 matrix instructions
+//   t_jr = S_jr kscale_j c_r + log2 vscale_j,  m_r = running maximum of t - 8
+//   x_jr = 2^(t_jr - m_r),  l_r += x_jr / vscale_j
+//   O^T += V^T X       [D x rows]
+// and o_r = O_r / l_r.  x carries V's scale in its exponent (the scales are powers of two),
+// so x <= 256 whatever the scales are, and K and V enter the tensor core as they are stored.
+//
+// Precision: E4M3 holds 4 significant bits.  A bf16 query (8 bits) is split in two pieces
+// of 4, hi = rn(q), lo = rn(16 (q - hi)) after a power of two brings the row's largest to
+// (224, 448]: exact for elements within 2^14 of it.  A probability is split the same way:
+// its 8 bits cost 2^-8 relative, half of what rounding the output to bf16 may.  The pieces are
+// separate columns of the same instruction, N = 2 rows, so 8 rows fill its smallest N of
+// 16 and the split is free there.  Accumulation is float32.
+//
+// How: the 128-token tiles of all units are laid end to end and cut evenly over a
+// persistent grid, two CTAs to an SM (each CTA finds its range from the device lengths by
+// itself); a unit that a cut splits leaves float32 partials which the join kernel adds.
+// Per CTA one warp issues the pages' bulk copies into a ring, one thread the matrix
+// instructions, four warps the softmax (a thread is a token, so scales and masks are one
+// per thread and the probabilities go to shared memory as bytes).  S is double buffered:
+// the next tile's S is computed under this one's softmax.
+#include "paged_mma.cuh"
+
+namespace kvs {
+namespace {
+
+using namespace pmma;
+
+constexpr int kTile = 128;               // tokens of a tile
+constexpr int kTileBlocks = kTile / kBlock;
+constexpr int kThreads = 192;            // 4 softmax warps, copies, matrix instructions
+constexpr int kCtasPerSm = 2;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTop = 8.f;              // the largest x is 2^8
+// Scales of the second pieces: the largest that keep them in range.  A query's first piece
+// is at most 448, where half a step is 16; a probability's 256, with half a step of 8 below it.
+constexpr float kLoQ = 16.f, kLoP = 32.f;
+
+// Tiles of request r's units (all KV heads alike) and their ranges.
+struct Unit {
+  int first, n;          // first packed row, query tokens handled
+  int hi0, lo0;          // the first query sees [lo0, hi0); the i-th [lo_i, hi0 + i)
+  int b0, nb, tiles;     // visible blocks of any of them
+};
+
+__device__ __forceinline__ Unit unit_of(const PagedAttend& a, int r, int most_tokens) {
+  Unit u;
+  u.first = r;
+  u.n = 1;
+  int n = 1;
+  if (a.row_start) {
+    u.first = __ldg(a.row_start + r);
+    n = __ldg(a.row_start + r + 1) - u.first;
+    u.n = u.first < 0 ? 0 : min(min(n, a.max_q_len), a.total_q - u.first);
+    if (u.n > most_tokens) u.n = 0;        // the prompt kernel's
+  }
+  const int len = min(max(__ldg(a.kv_len + r), 0), a.table_stride * kBlock);
+  const int p0 = len - n;                  // position of the first query; may be negative
+  u.hi0 = p0 + 1;
+  u.lo0 = a.window > 0 ? p0 + 1 - a.window : 0;
+  const int hi = max(p0 + u.n, 0);
+  u.b0 = max(u.lo0, 0) / kBlock;
+  u.nb = max((hi + kBlock - 1) / kBlock - u.b0, 0);
+  u.tiles = u.n > 0 ? max((u.nb + kTileBlocks - 1) / kTileBlocks, 1) : 0;
+  return u;
+}
+
+// A CTA's walk over its tiles, segment by segment (a segment: tiles of one unit).
+struct Walk {
+  int r, h;              // request, KV head
+  int t0, nt;            // the segment's tiles of the unit: [t0, t0 + nt)
+  int left;              // tiles of the CTA from here on
+  Unit u;
+  bool first, whole;
+  __device__ void clip() {
+    nt = min(u.tiles - t0, left);
+    whole = nt == u.tiles;
+  }
+  __device__ void next(const PagedAttend& a, int most_tokens) {
+    left -= nt;
+    first = false;
+    t0 = 0;
+    if (left <= 0) return;
+    if (++h == a.d.Hkv) {
+      h = 0;
+      do {
+        u = unit_of(a, ++r, most_tokens);
+      } while (u.tiles == 0);
+    }
+    clip();
+  }
+};
+
+// Sum over the requests of their units' tiles, and the prefix before `upto`, by every thread
+// of a block of `threads` (a multiple of 32, at most 256).
+__device__ void total_tiles(const PagedAttend& a, int most_tokens, int upto, int threads, long long* s_sum,
+                            long long& total, long long& before) {
+  long long all = 0, pre = 0;
+  for (int r = threadIdx.x; r < a.n_reqs; r += threads) {
+    const int t = unit_of(a, r, most_tokens).tiles;
+    all += t;
+    if (r < upto) pre += t;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    pre += __shfl_xor_sync(0xffffffffu, pre, o);
+  }
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) { s_sum[warp] = all; s_sum[8 + warp] = pre; }
+  __syncthreads();
+  total = before = 0;
+  for (int w = 0; w < threads / 32; ++w) { total += s_sum[w]; before += s_sum[8 + w]; }
+  __syncthreads();
+  total *= a.d.Hkv;
+  before *= a.d.Hkv;
+}
+
+template <int D, int RT>
+struct Cfg {
+  static constexpr int N = 2 * RT;                       // columns: both pieces of the rows
+  static constexpr int PAGE = 16 * D;                    // bytes of a page of K or V of one head
+  static constexpr int HALF = kTileBlocks * PAGE;        // K (or V) of a stage
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int Q = N * D, P = N * kTile;
+  static constexpr int MISC = 4096;
+  static constexpr int ROOM = 227 * 1024 / kCtasPerSm - 1024 - 2 * Q - P - MISC;
+  static constexpr int NS = ROOM / STAGE < 6 ? ROOM / STAGE : 6;
+  // an M of 128 reads a further 1 KB behind the last page of V for D = 64: Q is there
+  static constexpr int SMEM = NS * STAGE + 2 * Q + P + MISC + 1024;
+  static constexpr int TMEM = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 256;
+  static_assert(NS >= 2 && 3 * N <= TMEM && (SMEM + 1024) * kCtasPerSm <= 228 * 1024, "ring, TMEM, shared memory");
+};
+
+struct Misc {
+  uint64_t full[6], empty[6], s_ready[2], p_ready, o_done, q_ready, drain;
+  uint32_t tmem;
+  int token[32];         // query token of a row
+  int start_r, start_h, start_t;
+  long long sums[16];
+  float ks[6][kTileBlocks], ev[6][kTileBlocks], iv[6][kTileBlocks];   // of each stage's blocks
+  float qc[2][32];
+  float wmax[2][4][32];
+  float wsum[4][32];
+};
+static_assert(sizeof(Misc) <= 4096, "Misc");
+
+template <int D, int RT, bool MASS>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const PagedAttend a, const int most_tokens) {
+  using C = Cfg<D, RT>;
+  constexpr int N = C::N;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = smem;
+  uint8_t* sq = ring + C::NS * C::STAGE;
+  uint8_t* sp = sq + 2 * C::Q;
+  Misc& ms = *reinterpret_cast<Misc*>(sp + C::P);
+  const PagedDev& d = a.d;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  launch_dependents();
+  if (blockIdx.x == 0) report_rows(a, kThreads);
+  // this CTA's range
+  long long total, unused;
+  total_tiles(a, most_tokens, 0, kThreads, ms.sums, total, unused);
+  const long long ctas = min((long long)gridDim.x, total);      // every one of them has a tile
+  if (blockIdx.x >= ctas) return;
+  const long long begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+  // where it begins: the request whose units hold tile `begin`
+  {
+    long long at = 0;
+    for (int r0 = 0; r0 < a.n_reqs; r0 += kThreads) {
+      const int r = r0 + tid;
+      const int tiles = r < a.n_reqs ? unit_of(a, r, most_tokens).tiles : 0;
+      long long mine = (long long)tiles * d.Hkv, upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (lane == 31) ms.sums[warp] = upto;
+      __syncthreads();
+      long long base = at;
+      for (int w = 0; w < warp; ++w) base += ms.sums[w];
+      for (int w = 0; w < kThreads / 32; ++w) at += ms.sums[w];
+      upto += base;
+      if (begin >= upto - mine && begin < upto) {
+        const int off = (int)(begin - (upto - mine));
+        ms.start_r = r;
+        ms.start_h = off / tiles;
+        ms.start_t = off % tiles;
+      }
+      __syncthreads();
+      if (at > begin) break;
+    }
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(smem_u32(&ms.full[i]), 1);
+      mbar_init(smem_u32(&ms.empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ms.s_ready[0]), 1);
+    mbar_init(smem_u32(&ms.s_ready[1]), 1);
+    mbar_init(smem_u32(&ms.p_ready), 4);
+    mbar_init(smem_u32(&ms.o_done), 1);
+    mbar_init(smem_u32(&ms.q_ready), 4);
+    mbar_init(smem_u32(&ms.drain), 1);
+    mbar_fence_init();
+  }
+  if (tid < RT) ms.token[tid] = tid / d.G;
+  if (warp == 5) {
+    umma::alloc(smem_u32(&ms.tmem), C::TMEM);
+    umma::relinquish();
+  }
+  umma::fence_before();
+  __syncthreads();
+  umma::fence_after();
+  const uint32_t tmem = ms.tmem, t_o = tmem + 2 * N;
+  Walk w;
+  w.r = ms.start_r;
+  w.h = ms.start_h;
+  w.t0 = ms.start_t;
+  w.left = (int)(end - begin);
+  w.first = true;
+  w.u = unit_of(a, w.r, most_tokens);
+  w.clip();
+
+  if (warp == 4) {
+    // ---- copies: lane j < 8 has block j of the tile
+    const uint64_t policy = evict_first_policy();
+    const uint8_t* kbase = d.k + a.layer * d.layer_bytes;
+    const uint8_t* vbase = d.v + a.layer * d.layer_bytes;
+    const float2* sbase = d.scales + a.layer * d.layer_scales;
+    int count = 0;
+    bool ok = true;
+    while (w.left > 0 && ok) {
+      const int32_t* row = a.table + (size_t)w.r * a.table_stride;
+      auto fetch = [&](int t, int& nb, int& page, float2& sc) {
+        const int b = w.u.b0 + t * kTileBlocks;
+        nb = max(0, min(kTileBlocks, w.u.b0 + w.u.nb - b));
+        page = -1;
+        sc = make_float2(0.f, 1.f);
+        if (lane < nb) {
+          page = __ldg(row + b + lane);
+          if (page < 0 || page >= d.num_pages) {
+            paged_error(d, kErrState);
+            page = 0;
+          } else {
+            sc = __ldg(sbase + (size_t)page * d.Hkv + w.h);
+            sc.x = fmaxf(sc.x, exp2_int(kScaleMinExp));      // a page that nothing was stored in has 0
+            sc.y = fmaxf(sc.y, exp2_int(kScaleMinExp));
+          }
+        }
+      };
+      int nb, page;
+      float2 sc;
+      fetch(w.t0, nb, page, sc);
+      for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
+        const int st = count % C::NS;
+        if (count >= C::NS) ok = mbar_wait(smem_u32(&ms.empty[st]), (count / C::NS - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t full = smem_u32(&ms.full[st]);
+        const uint32_t dst = smem_u32(ring + st * C::STAGE);
+        // the last odd block's neighbour in V is read by the matrix instruction (with
+        // probability 0): it gets the first block's values, which are finite
+        const int odd = nb & 1;
+        if (lane == 0) mbar_expect(full, (2 * nb + odd) * C::PAGE);
+        __syncwarp();
+        const int page0 = __shfl_sync(0xffffffffu, page, 0);
+        if (lane < nb) {
+          const size_t at = ((size_t)page * d.Hkv + w.h) * C::PAGE;
+          bulk_load(dst + lane * C::PAGE, kbase + at, C::PAGE, full, policy);
+          bulk_load(dst + C::HALF + lane * C::PAGE, vbase + at, C::PAGE, full, policy);
+        } else if (lane == nb && odd) {
+          bulk_load(dst + C::HALF + lane * C::PAGE, vbase + ((size_t)page0 * d.Hkv + w.h) * C::PAGE, C::PAGE, full, policy);
+        }
+        if (lane < kTileBlocks) {
+          const float ev = (float)((__float_as_int(sc.y) >> 23) - 127);
+          ms.ks[st][lane] = sc.x;                           // 0: nothing of this block is visible
+          ms.ev[st][lane] = ev;
+          ms.iv[st][lane] = exp2_int(-(int)ev);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+        if (t + 1 < w.t0 + w.nt) fetch(t + 1, nb, page, sc);
+      }
+      if (ok) w.next(a, most_tokens);
+    }
+    if (!ok && lane == 0) paged_error(d, kErrTimeout);
+    // copies still in flight land before the CTA ends
+    for (int i = max(0, count - C::NS); i < count; ++i) mbar_wait(smem_u32(&ms.full[i % C::NS]), (i / C::NS) & 1);
+  } else if (warp == 5) {
+    // ---- matrix instructions, by one thread
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_e4m3(128, N);
+      int count = 0, seg = 0;
+      bool ok = true;
+      auto pv = [&](int i, int nb, bool fresh) {            // tile number i of the CTA
+        const int st = i % C::NS;
+        umma::fence_after();
+        const uint32_t av = smem_u32(ring + st * C::STAGE + C::HALF), bp = smem_u32(sp);
+        const int steps = (nb + 1) / 2;
+        for (int k = 0; k < steps; ++k)
+          mma_e4m3(t_o, desc(av + k * 2 * C::PAGE, C::PAGE, 128), desc(bp + k * 2 * N * 16, N * 16, 128), id,
+                   !(fresh && k == 0));
+        umma::commit(smem_u32(&ms.empty[st]));
+        umma::commit(smem_u32(&ms.o_done));
+      };
+      while (w.left > 0 && ok) {
+        ok = mbar_wait(smem_u32(&ms.q_ready), seg & 1);
+        const uint32_t bq = smem_u32(sq + (seg & 1) * C::Q);
+        int nb_before = 0;
+        for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
+          const int st = count % C::NS, nb = max(0, min(kTileBlocks, w.u.nb - t * kTileBlocks));
+          ok = mbar_wait(smem_u32(&ms.full[st]), (count / C::NS) & 1);
+          if (!ok) break;
+          umma::fence_after();
+          const uint32_t ak = smem_u32(ring + st * C::STAGE);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            mma_e4m3(tmem + (count & 1) * N, desc(ak + k * 256, 128, 8 * D), desc(bq + k * 256, 128, 8 * D), id, k > 0);
+          umma::commit(smem_u32(&ms.s_ready[count & 1]));
+          if (t > w.t0) {
+            ok = mbar_wait(smem_u32(&ms.p_ready), (count - 1) & 1);
+            if (!ok) break;
+            pv(count - 1, nb_before, t - 1 == w.t0);
+          }
+          nb_before = nb;
+        }
+        if (ok) ok = mbar_wait(smem_u32(&ms.p_ready), (count - 1) & 1);
+        if (!ok) break;
+        pv(count - 1, nb_before, w.nt == 1);
+        ++seg;
+        w.next(a, most_tokens);
+      }
+      if (!ok) paged_error(d, kErrTimeout);
+      umma::commit(smem_u32(&ms.drain));
+      mbar_wait(smem_u32(&ms.drain), 0);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: thread = token of the tile, then = dimension of the output
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const float qk = kLog2e * rsqrtf((float)D);
+    // the rows' queries as two E4M3 pieces; TPR threads to a row
+    auto load_q = [&](const Walk& x, int buf) {
+      constexpr int TPR = 128 / RT, E = D / TPR;
+      const int row = tid / TPR, part = tid % TPR;
+      float v[E];
+      float amax = 0.f;
+      const bool live = row < x.u.n * d.G;
+      if (live) {
+        const size_t at = ((size_t)(x.u.first + row / d.G) * d.Hq + x.h * d.G + row % d.G) * D + part * E;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at;
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+          const uint2 raw = __ldg(reinterpret_cast<const uint2*>(src + i));
+          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.x));
+          const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.y));
+          v[i] = f.x; v[i + 1] = f.y; v[i + 2] = g.x; v[i + 3] = g.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+      for (int o = TPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int e = scale_exp(amax);
+      const float up = exp2_int(-e);
+      uint8_t* base = sq + buf * C::Q;
+#pragma unroll
+      for (int i = 0; i < E; i += 4) {
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float f = v[i + 2 * u] * up, g = v[i + 2 * u + 1] * up;
+          hi[u] = float2_to_e4m3x2(f, g);
+          const float2 back = e4m3x2_to_float2(hi[u]);
+          lo[u] = float2_to_e4m3x2((f - back.x) * kLoQ, (g - back.y) * kLoQ);
+        }
+        const int dim = part * E + i;
+        *reinterpret_cast<uint32_t*>(base + k_code(D, row, dim)) = hi[0] | hi[1] << 16;
+        *reinterpret_cast<uint32_t*>(base + k_code(D, row + RT, dim)) = lo[0] | lo[1] << 16;
+      }
+      if (part == 0) ms.qc[buf][row] = live ? exp2_int(e) * qk : 0.f;
+      umma::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready));
+    };
+    load_q(w, 0);
+    named_sync(1, 128);                                    // qc of all rows
+    int count = 0, seg = 0;
+    bool ok = true;
+    while (w.left > 0 && ok) {
+      float m[RT], l[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
+      const float* qc = ms.qc[seg & 1];
+      const int rows = w.u.n * d.G;
+      for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
+        const int st = count % C::NS;
+        ok = mbar_wait(smem_u32(&ms.s_ready[count & 1]), (count >> 1) & 1);
+        // the scales came with the stage: its barrier has completed, this orders the reads
+        if (ok) ok = mbar_wait(smem_u32(&ms.full[st]), (count / C::NS) & 1);
+        umma::fence_after();
+        const int blk = tid >> 4, b = w.u.b0 + t * kTileBlocks;
+        const float ks = ms.ks[st][blk], ev = ms.ev[st][blk], iv = ms.iv[st][blk];
+        const int pos = b * kBlock + tid;
+        float x[RT];
+        {
+          float s[N];
+          const uint32_t ts = tmem + (count & 1) * N + lanes;
+#pragma unroll
+          for (int c = 0; c < N; c += 16) ld16(ts + c, s + c);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) x[r] = fmaf(fmaf(s[r + RT], 1.f / kLoQ, s[r]), ks * qc[r], ev);
+        }
+        if (w.u.n == 1) {
+          const bool seen = ks > 0.f && pos < w.u.hi0 && pos >= w.u.lo0;
+#pragma unroll
+          for (int r = 0; r < RT; ++r) x[r] = seen ? x[r] : -INFINITY;
+        } else {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const int i = ms.token[r];
+            const bool seen = ks > 0.f && pos < w.u.hi0 + i && (a.window == 0 || pos >= w.u.lo0 + i);
+            x[r] = seen ? x[r] : -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          float top = x[r];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (lane == (r & 31)) ms.wmax[count & 1][warp][r] = top;
+        }
+        named_sync(1, 128);
+        bool grew = false;
+        float f[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const float top = fmaxf(fmaxf(ms.wmax[count & 1][0][r], ms.wmax[count & 1][1][r]),
+                                  fmaxf(ms.wmax[count & 1][2][r], ms.wmax[count & 1][3][r])) - kTop;
+          const float now = fmaxf(m[r], top);
+          f[r] = 1.f;
+          if (now > m[r]) {
+            f[r] = ex2(m[r] - now);
+            grew = true;
+          }
+          m[r] = now;
+          x[r] = now > -INFINITY ? ex2(x[r] - now) : 0.f;
+          l[r] = fmaf(l[r], f[r], x[r] * iv);
+        }
+        if (MASS) {
+          // the blocks' sums, as log2, for the rows of one token
+          float keep = 0.f, ref = 0.f;
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            float s = x[r] * iv;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if ((lane & 15) == (r & 15)) { keep = s; ref = m[r]; }
+            if ((r & 15) == 15 || r == RT - 1) {
+              const int row = (r & ~15) + (lane & 15);
+              if (row <= r && row < rows && b + blk < w.u.b0 + w.u.nb)
+                a.blk[((size_t)w.r * a.table_stride + b + blk) * d.Hq + w.h * d.G + row] = __log2f(keep) + ref;
+            }
+          }
+        }
+        // the previous product is done with the probabilities' buffer and the output
+        if (ok && count > 0) ok = mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
+        umma::fence_after();
+        if (grew && t > w.t0) {                            // the same in all threads
+#pragma unroll
+          for (int c = 0; c < N; c += 16) {
+            float o[16];
+            ld16(t_o + lanes + c, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= f[(c + i) % RT];
+            st16(t_o + lanes + c, o);
+          }
+          wait_st();
+        }
+        uint8_t* p = sp + (tid >> 4) * (N * 16) + (tid & 15);
+#pragma unroll
+        for (int r = 0; r < RT; r += 2) {
+          const uint32_t hi = float2_to_e4m3x2(x[r], x[r + 1]);
+          const float2 back = e4m3x2_to_float2(hi);
+          const uint32_t lo = float2_to_e4m3x2((x[r] - back.x) * kLoP, (x[r + 1] - back.y) * kLoP);
+          p[r * 16] = (uint8_t)hi;
+          p[(r + 1) * 16] = (uint8_t)(hi >> 8);
+          p[(r + RT) * 16] = (uint8_t)lo;
+          p[(r + RT + 1) * 16] = (uint8_t)(lo >> 8);
+        }
+        umma::fence_async_smem();
+        umma::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready));
+      }
+      if (!ok) break;
+      // the sums over the tokens; the next segment's queries while the last product runs
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+        if (lane == (r & 31)) ms.wsum[warp][r] = l[r];
+      }
+      Walk x = w;
+      x.next(a, most_tokens);
+      if (x.left > 0) load_q(x, (seg + 1) & 1);
+      named_sync(1, 128);
+      ok = mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
+      umma::fence_after();
+      if (!ok) break;
+      float o[RT];
+      {
+        float s[N];
+#pragma unroll
+        for (int c = 0; c < N; c += 16) ld16(t_o + lanes + c, s + c);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) o[r] = fmaf(s[r + RT], 1.f / kLoP, s[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) l[r] = ms.wsum[0][r] + ms.wsum[1][r] + ms.wsum[2][r] + ms.wsum[3][r];
+      if (w.whole) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          if (r < rows && tid < D)
+            out[((size_t)(w.u.first + r / d.G) * d.Hq + w.h * d.G + r % d.G) * D + tid] =
+                __float2bfloat16_rn(l[r] > 0.f ? o[r] / l[r] : 0.f);
+          if (MASS && r < rows && tid == r) a.lse[(size_t)w.r * d.Hq + w.h * d.G + r] = m[r] + log2f(l[r]);
+        }
+      } else {
+        const size_t rec = (size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * RT;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          if (r < rows) {
+            if (tid < D) a.part_o[(rec + r) * D + tid] = o[r];
+            if (tid == r) a.part_ml[rec + r] = make_float2(m[r], l[r]);
+          }
+      }
+      umma::fence_before();
+      ++seg;
+      w = x;
+    }
+    if (!ok && lane == 0) paged_error(d, kErrTimeout);
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 5) {
+    umma::fence_after();
+    umma::dealloc(tmem, C::TMEM);
+  }
+}
+
+// CTA of `ctas` <= total that holds tile x of `total`: the last one that begins at or before it.
+__device__ __forceinline__ int cta_of(long long x, long long total, int ctas) {
+  return (int)(((x + 1) * ctas + total - 1) / total) - 1;
+}
+
+// Adds the partials of the units that a cut splits: a CTA per (unit, row).
+template <int D, int RT, bool MASS>
+__global__ void __launch_bounds__(128) join_kernel(const PagedAttend a, const int most_tokens, const int grid) {
+  __shared__ long long sums[16];
+  const PagedDev& d = a.d;
+  const int unit = blockIdx.x, r = unit / d.Hkv, h = unit % d.Hkv, row = blockIdx.y, tid = threadIdx.x;
+  const Unit u = unit_of(a, r, most_tokens);
+  long long total = 1, before = 0;
+  if (u.tiles > 0 && row < u.n * d.G) total_tiles(a, most_tokens, r, 128, sums, total, before);
+  const long long off = before + (long long)h * u.tiles;
+  const int ctas = (int)min((long long)grid, total);
+  const int c0 = cta_of(off, total, ctas), c1 = u.tiles ? cta_of(off + u.tiles - 1, total, ctas) : c0;
+  wait_previous();
+  if (u.tiles == 0 || row >= u.n * d.G || c0 == c1) return;
+  auto rec_of = [&](int c) {
+    const bool first = off <= total * c / ctas;            // the unit is the CTA's first
+    return (size_t)(2 * c + (first ? 0 : 1)) * RT + row;
+  };
+  float top = -INFINITY;
+  for (int c = c0; c <= c1; ++c) top = fmaxf(top, a.part_ml[rec_of(c)].x);
+  const float ref = top > -INFINITY ? top : 0.f;
+  float sum = 0.f, acc = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const size_t rec = rec_of(c);
+    const float2 ml = a.part_ml[rec];
+    const float f = ex2(ml.x - ref);
+    sum = fmaf(ml.y, f, sum);
+    if (tid < D) acc = fmaf(a.part_o[rec * D + tid], f, acc);
+  }
+  const int hq = h * d.G + row % d.G;
+  if (tid < D)
+    static_cast<__nv_bfloat16*>(a.out)[((size_t)(u.first + row / d.G) * d.Hq + hq) * D + tid] =
+        __float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f);
+  if (MASS && tid == 0) a.lse[(size_t)r * d.Hq + hq] = top + log2f(sum);
+}
+
+template <int D, int RT, bool MASS>
+cudaError_t launch(const PagedAttend& a, int most_tokens, int grid, cudaStream_t st) {
+  using C = Cfg<D, RT>;
+  static std::atomic<unsigned long long> opted{0};
+  cudaError_t e = smem_optin_once(opted, decode_kernel<D, RT, MASS>, C::SMEM);
+  if (e != cudaSuccess) return e;
+  decode_kernel<D, RT, MASS><<<grid, kThreads, C::SMEM, st>>>(a, most_tokens);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  const int rows = (a.row_start ? (a.max_q_len < most_tokens ? a.max_q_len : most_tokens) : 1) * a.d.G;
+  cfg.gridDim = dim3(a.n_reqs * a.d.Hkv, rows);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, RT, MASS>, a, most_tokens, grid);
+}
+
+template <int D>
+cudaError_t launch_d(const PagedAttend& a, int rows, int grid, cudaStream_t st) {
+  const int most = rows / a.d.G;
+  const bool mass = a.mass != nullptr;
+  switch (rows) {
+    case 8: return mass ? launch<D, 8, true>(a, most, grid, st) : launch<D, 8, false>(a, most, grid, st);
+    case 16: return mass ? launch<D, 16, true>(a, most, grid, st) : launch<D, 16, false>(a, most, grid, st);
+    default: return mass ? launch<D, 32, true>(a, most, grid, st) : launch<D, 32, false>(a, most, grid, st);
+  }
+}
+
+}  // namespace
+
+int paged_decode_ctas_per_sm() { return kCtasPerSm; }
+
+// rows: 8, 16 or 32, query rows of a unit (requests with more tokens than rows / G are left
+// to the prompt kernel).
+cudaError_t launch_paged_decode(const PagedAttend& a, int rows, int grid, cudaStream_t st) {
+  return a.d.D == 64 ? launch_d<64>(a, rows, grid, st) : launch_d<128>(a, rows, grid, st);
+}
+
+}  // namespace kvs

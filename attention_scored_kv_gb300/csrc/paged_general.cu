@@ -240,13 +240,7 @@ __global__ void __launch_bounds__(kWarps * 32) mass_kernel(const PagedAttend a) 
   }
 }
 
-// Reports a call whose device lengths pass what the host was told.
-__global__ void check_rows_kernel(const PagedAttend a) {
-  for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < a.n_reqs; r += gridDim.x * blockDim.x) {
-    const int lo = a.row_start[r], hi = a.row_start[r + 1];
-    if (hi - lo > a.max_q_len || hi > a.total_q || lo < 0 || hi < lo) paged_error(a.d, kErrCapacity);
-  }
-}
+__global__ void check_rows_kernel(const PagedAttend a) { report_rows(a, blockDim.x); }
 
 template <int DT, int D>
 cudaError_t general_d(const PagedAttend& a, cudaStream_t st) {
@@ -260,7 +254,7 @@ cudaError_t general_d(const PagedAttend& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_paged_general(const PagedAttend& a, cudaStream_t st) {
-  if (a.row_start) check_rows_kernel<<<(unsigned)cdiv64(a.n_reqs, 256), 256, 0, st>>>(a);
+  if (a.row_start) check_rows_kernel<<<1, 256, 0, st>>>(a);
   const bool b = a.d.in_dtype == KVS_BF16;
   switch (a.d.D) {
     case 16: return b ? general_d<KVS_BF16, 16>(a, st) : general_d<KVS_F32, 16>(a, st);

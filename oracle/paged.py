@@ -101,7 +101,9 @@ class Pages:
     def attend(self, q, table, kv_len, row_start=None, window=0):
         """dict: out [rows, hq, d]; spread, the same with |v| (the scale of what rounding a
         probability costs); reach [rows, hq], the largest sum |q k| / sqrt(D) over a row's
-        entries (the scale of a logit's error); mass [n, stride] for single-token rows."""
+        entries (the scale of a logit's error); floor, max_j(weight * V scale) * sum_j |V code|
+        (the scale of what a probability's smallest step costs); mass [n, stride] for
+        single-token rows."""
         q = np.asarray(q, np.float64)
         rows, hq, d = q.shape
         table = np.asarray(table)
@@ -110,7 +112,7 @@ class Pages:
         g = hq // hkv
         row_start = np.arange(n + 1) if row_start is None else np.asarray(row_start)
         out, spread, reach = np.zeros((rows, hq, d)), np.zeros((rows, hq, d)), np.zeros((rows, hq))
-        mass = np.zeros((n, stride))
+        mass, floor = np.zeros((n, stride)), np.zeros((rows, hq, d))
         for r in range(n):
             length = min(max(int(kv_len[r]), 0), stride * PAGE)
             pages = table[r, :-(-length // PAGE)]
@@ -118,6 +120,7 @@ class Pages:
             pages = np.where((pages >= 0) & (pages < self.num_pages), pages, 0)
             k, v = ((c[pages] * z[pages][:, None, :, None]).reshape(-1, hkv, d)[:length]
                     for c, z in zip(self.codes, self.scales))
+            vs = self.scales[1][pages].repeat(PAGE, axis=0)[:length]
             nq = int(row_start[r + 1] - row_start[r])
             for i in range(nq):
                 t = int(row_start[r]) + i
@@ -137,8 +140,10 @@ class Pages:
                 wg = w.reshape(hkv, g, -1)
                 out[t] = (wg @ vh.transpose(1, 0, 2)).reshape(hq, d)
                 spread[t] = (wg @ np.abs(vh).transpose(1, 0, 2)).reshape(hq, d)
+                codes = np.repeat((np.abs(vh) / vs[seen][:, :, None]).sum(0), g, axis=0)       # [hq, d]
+                floor[t] = (w * np.repeat(vs[seen].T, g, axis=0)).max(-1)[:, None] * codes
                 if nq == 1:
                     blocks = np.zeros((hq, stride))
                     np.add.at(blocks.T, j[seen] // PAGE, w.T)
                     mass[r] = blocks.max(0)
-        return {"out": out, "spread": spread, "reach": reach, "mass": mass}
+        return {"out": out, "spread": spread, "reach": reach, "floor": floor, "mass": mass}
