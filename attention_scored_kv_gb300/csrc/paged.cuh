@@ -49,11 +49,10 @@ struct PagedAttend {
 // How a call runs: a pure function of host-known sizes, so that the scratch size and the
 // launch agree.
 struct PagedAttendPlan {
-  bool tensor;
+  enum Kernel { kGeneral, kDecode, kPrompt } kernel;
   int splits;              // general kernel
-  int rows;                // tensor decode kernel: query rows of a unit (0 = not launched)
-  bool prompt;             // tensor prompt kernel launched
-  int grid;                // tensor decode kernel
+  int rows;                // decode kernel: query rows of a unit
+  int grid;                // decode and prompt kernels
   size_t part_o, part_ml, blk, lse, total;   // scratch offsets
 };
 
@@ -122,6 +121,8 @@ cudaError_t launch_paged_gather(const PagedDev& d, int layer, int n_rows, const 
                                 cudaStream_t st);
 int paged_decode_ctas_per_sm();
 cudaError_t launch_paged_decode(const PagedAttend& a, int rows, int grid, cudaStream_t st);
+int paged_prompt_rows();
+cudaError_t launch_paged_prompt(const PagedAttend& a, int grid, cudaStream_t st);
 cudaError_t launch_paged_general(const PagedAttend& a, cudaStream_t st);
 cudaError_t launch_paged_mass(const PagedAttend& a, cudaStream_t st);
 

@@ -119,13 +119,18 @@ PagedAttendPlan plan_attend(const kvs_paged* pc, int n_reqs, int stride, int tot
   const PagedDev& d = pc->dev;
   size_t recs = 0;
   const long long need = (long long)max_q_len * d.G;       // query rows of a unit
-  p.tensor = pc->tensor && need <= 32;
-  if (p.tensor) {
+  p.splits = 1;
+  if (pc->tensor && need <= 32) {
+    p.kernel = PagedAttendPlan::kDecode;
     p.rows = need <= 8 ? 8 : need <= 16 ? 16 : 32;
     p.grid = paged_decode_ctas_per_sm() * pc->sms;
-    p.splits = 1;
     recs = (size_t)2 * p.grid * p.rows;                    // a CTA leaves at most two partials
+  } else if (pc->tensor && !mass) {
+    p.kernel = PagedAttendPlan::kPrompt;
+    p.grid = pc->sms;
+    recs = (size_t)2 * p.grid * paged_prompt_rows();
   } else {
+    p.kernel = PagedAttendPlan::kGeneral;
     // a part per idle CTA, four CTAs to an SM, no part under a page a warp
     const long long units = (long long)total_q * d.Hkv;
     long long want = units > 0 ? (long long)pc->sms * 4 / units : 1;
@@ -359,7 +364,9 @@ kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const 
   a.lse = d_block_mass_opt ? reinterpret_cast<float*>(s + p.lse) : nullptr;
   a.splits = p.splits;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = p.tensor ? launch_paged_decode(a, p.rows, p.grid, cs) : launch_paged_general(a, cs);
+  cudaError_t e = p.kernel == PagedAttendPlan::kDecode   ? launch_paged_decode(a, p.rows, p.grid, cs)
+                  : p.kernel == PagedAttendPlan::kPrompt ? launch_paged_prompt(a, p.grid, cs)
+                                                         : launch_paged_general(a, cs);
   if (e == cudaSuccess && a.mass) e = launch_paged_mass(a, cs);
   return cuda_ok(pc, e, "attend");
 }

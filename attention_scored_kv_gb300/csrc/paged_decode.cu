@@ -48,7 +48,7 @@ struct Unit {
   int b0, nb, tiles;     // visible blocks of any of them
 };
 
-__device__ __forceinline__ Unit unit_of(const PagedAttend& a, int r, int most_tokens) {
+__device__ __forceinline__ Unit unit_of(const PagedAttend& a, int r) {
   Unit u;
   u.first = r;
   u.n = 1;
@@ -57,7 +57,6 @@ __device__ __forceinline__ Unit unit_of(const PagedAttend& a, int r, int most_to
     u.first = __ldg(a.row_start + r);
     n = __ldg(a.row_start + r + 1) - u.first;
     u.n = u.first < 0 ? 0 : min(min(n, a.max_q_len), a.total_q - u.first);
-    if (u.n > most_tokens) u.n = 0;        // the prompt kernel's
   }
   const int len = min(max(__ldg(a.kv_len + r), 0), a.table_stride * kBlock);
   const int p0 = len - n;                  // position of the first query; may be negative
@@ -81,7 +80,7 @@ struct Walk {
     nt = min(u.tiles - t0, left);
     whole = nt == u.tiles;
   }
-  __device__ void next(const PagedAttend& a, int most_tokens) {
+  __device__ void next(const PagedAttend& a) {
     left -= nt;
     first = false;
     t0 = 0;
@@ -89,7 +88,7 @@ struct Walk {
     if (++h == a.d.Hkv) {
       h = 0;
       do {
-        u = unit_of(a, ++r, most_tokens);
+        u = unit_of(a, ++r);
       } while (u.tiles == 0);
     }
     clip();
@@ -98,11 +97,11 @@ struct Walk {
 
 // Sum over the requests of their units' tiles, and the prefix before `upto`, by every thread
 // of a block of `threads` (a multiple of 32, at most 256).
-__device__ void total_tiles(const PagedAttend& a, int most_tokens, int upto, int threads, long long* s_sum,
+__device__ void total_tiles(const PagedAttend& a, int upto, int threads, long long* s_sum,
                             long long& total, long long& before) {
   long long all = 0, pre = 0;
   for (int r = threadIdx.x; r < a.n_reqs; r += threads) {
-    const int t = unit_of(a, r, most_tokens).tiles;
+    const int t = unit_of(a, r).tiles;
     all += t;
     if (r < upto) pre += t;
   }
@@ -151,7 +150,7 @@ struct Misc {
 static_assert(sizeof(Misc) <= 4096, "Misc");
 
 template <int D, int RT, bool MASS>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const PagedAttend a, const int most_tokens) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const PagedAttend a) {
   using C = Cfg<D, RT>;
   constexpr int N = C::N;
   extern __shared__ uint8_t smem_raw[];
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
   if (blockIdx.x == 0) report_rows(a, kThreads);
   // this CTA's range
   long long total, unused;
-  total_tiles(a, most_tokens, 0, kThreads, ms.sums, total, unused);
+  total_tiles(a, 0, kThreads, ms.sums, total, unused);
   const long long ctas = min((long long)gridDim.x, total);      // every one of them has a tile
   if (blockIdx.x >= ctas) return;
   const long long begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
     long long at = 0;
     for (int r0 = 0; r0 < a.n_reqs; r0 += kThreads) {
       const int r = r0 + tid;
-      const int tiles = r < a.n_reqs ? unit_of(a, r, most_tokens).tiles : 0;
+      const int tiles = r < a.n_reqs ? unit_of(a, r).tiles : 0;
       long long mine = (long long)tiles * d.Hkv, upto = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
   w.t0 = ms.start_t;
   w.left = (int)(end - begin);
   w.first = true;
-  w.u = unit_of(a, w.r, most_tokens);
+  w.u = unit_of(a, w.r);
   w.clip();
 
   if (warp == 4) {
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
         if (lane == 0) mbar_arrive(full);
         if (t + 1 < w.t0 + w.nt) fetch(t + 1, nb, page, sc);
       }
-      if (ok) w.next(a, most_tokens);
+      if (ok) w.next(a);
     }
     if (!ok && lane == 0) paged_error(d, kErrTimeout);
     // copies still in flight land before the CTA ends
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
         if (!ok) break;
         pv(count - 1, nb_before, w.nt == 1);
         ++seg;
-        w.next(a, most_tokens);
+        w.next(a);
       }
       if (!ok) paged_error(d, kErrTimeout);
       umma::commit(smem_u32(&ms.drain));
@@ -514,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
         if (lane == (r & 31)) ms.wsum[warp][r] = l[r];
       }
       Walk x = w;
-      x.next(a, most_tokens);
+      x.next(a);
       if (x.left > 0) load_q(x, (seg + 1) & 1);
       named_sync(1, 128);
       ok = mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
@@ -569,13 +568,13 @@ __device__ __forceinline__ int cta_of(long long x, long long total, int ctas) {
 
 // Adds the partials of the units that a cut splits: a CTA per (unit, row).
 template <int D, int RT, bool MASS>
-__global__ void __launch_bounds__(128) join_kernel(const PagedAttend a, const int most_tokens, const int grid) {
+__global__ void __launch_bounds__(128) join_kernel(const PagedAttend a, const int grid) {
   __shared__ long long sums[16];
   const PagedDev& d = a.d;
   const int unit = blockIdx.x, r = unit / d.Hkv, h = unit % d.Hkv, row = blockIdx.y, tid = threadIdx.x;
-  const Unit u = unit_of(a, r, most_tokens);
+  const Unit u = unit_of(a, r);
   long long total = 1, before = 0;
-  if (u.tiles > 0 && row < u.n * d.G) total_tiles(a, most_tokens, r, 128, sums, total, before);
+  if (u.tiles > 0 && row < u.n * d.G) total_tiles(a, r, 128, sums, total, before);
   const long long off = before + (long long)h * u.tiles;
   const int ctas = (int)min((long long)grid, total);
   const int c0 = cta_of(off, total, ctas), c1 = u.tiles ? cta_of(off + u.tiles - 1, total, ctas) : c0;
@@ -605,16 +604,16 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedAttend a, const in
 }
 
 template <int D, int RT, bool MASS>
-cudaError_t launch(const PagedAttend& a, int most_tokens, int grid, cudaStream_t st) {
+cudaError_t launch(const PagedAttend& a, int grid, cudaStream_t st) {
   using C = Cfg<D, RT>;
   static std::atomic<unsigned long long> opted{0};
   cudaError_t e = smem_optin_once(opted, decode_kernel<D, RT, MASS>, C::SMEM);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, RT, MASS><<<grid, kThreads, C::SMEM, st>>>(a, most_tokens);
+  decode_kernel<D, RT, MASS><<<grid, kThreads, C::SMEM, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int rows = (a.row_start ? (a.max_q_len < most_tokens ? a.max_q_len : most_tokens) : 1) * a.d.G;
+  const int rows = a.max_q_len * a.d.G;
   cfg.gridDim = dim3(a.n_reqs * a.d.Hkv, rows);
   cfg.blockDim = dim3(128);
   cfg.stream = st;
@@ -623,17 +622,16 @@ cudaError_t launch(const PagedAttend& a, int most_tokens, int grid, cudaStream_t
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, RT, MASS>, a, most_tokens, grid);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, RT, MASS>, a, grid);
 }
 
 template <int D>
 cudaError_t launch_d(const PagedAttend& a, int rows, int grid, cudaStream_t st) {
-  const int most = rows / a.d.G;
   const bool mass = a.mass != nullptr;
   switch (rows) {
-    case 8: return mass ? launch<D, 8, true>(a, most, grid, st) : launch<D, 8, false>(a, most, grid, st);
-    case 16: return mass ? launch<D, 16, true>(a, most, grid, st) : launch<D, 16, false>(a, most, grid, st);
-    default: return mass ? launch<D, 32, true>(a, most, grid, st) : launch<D, 32, false>(a, most, grid, st);
+    case 8: return mass ? launch<D, 8, true>(a, grid, st) : launch<D, 8, false>(a, grid, st);
+    case 16: return mass ? launch<D, 16, true>(a, grid, st) : launch<D, 16, false>(a, grid, st);
+    default: return mass ? launch<D, 32, true>(a, grid, st) : launch<D, 32, false>(a, grid, st);
   }
 }
 
@@ -641,8 +639,7 @@ cudaError_t launch_d(const PagedAttend& a, int rows, int grid, cudaStream_t st) 
 
 int paged_decode_ctas_per_sm() { return kCtasPerSm; }
 
-// rows: 8, 16 or 32, query rows of a unit (requests with more tokens than rows / G are left
-// to the prompt kernel).
+// rows: 8, 16 or 32, at least max_q_len * G.
 cudaError_t launch_paged_decode(const PagedAttend& a, int rows, int grid, cudaStream_t st) {
   return a.d.D == 64 ? launch_d<64>(a, rows, grid, st) : launch_d<128>(a, rows, grid, st);
 }

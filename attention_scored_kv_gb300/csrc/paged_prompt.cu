@@ -1,0 +1,750 @@
+// Tensor-core attention over the paged cache for many query rows: prompt chunks, and calls
+// with more rows to a request than the decode kernel takes (bf16 queries, head_dim 64 or 128).
+//
+// A unit is a (request, KV head) and up to 256 query rows (tokens x heads of the group, two
+// tiles A and B of 128), which share every K and V they read.  Per 128 cached tokens:
+//   S = Q K^T        two pieces of Q (4 significant bits each) as one contraction of 2 D,
+//                    E4M3 x E4M3, K as it is stored
+//   t = S kscale c_r + log2 vscale,  m_r: a maximum that moves only by steps of 2^8 or more
+//   x = 2^(t - m_r + 6),  l_r += x / vscale,  O += X V      f16 x f16
+// and o = O / l.  The scales are powers of two, so V's rides in x's exponent and V's codes
+// are exact in f16; x <= 2^14 fits f16, whose 11 bits are finer than the output's 8.
+// Queries: exact down to 2^-10 of the row's largest element, an error of 2^-19 of the
+// largest below that.
+//
+// How: work is cut as in the decode kernel: the 128-token tiles of all units laid end to
+// end and split evenly over one CTA per SM, partials of split units added by a join
+// kernel.  That also balances causal rows, whose units differ in length, and feeds all
+// SMs when rows are few and the context is long.
+// Per CTA: one warp copies K pages into a ring, four warps convert V's codes to f16 operand
+// rows (a page's rows are its operand rows, so it is load, convert, store), one thread
+// issues the matrix instructions, and two groups of four warps do the softmax of A and B, a
+// thread to a row, so that no row statistic crosses threads.  The matrix thread works on
+// one tile while the other's softmax runs: S(A, j+1) and O(A) += X(A, j) V while B's
+// exponentials are computed, then the reverse.
+#include "paged_mma.cuh"
+
+namespace kvs {
+namespace {
+
+using namespace pmma;
+
+constexpr int kTile = 128, kTileBlocks = kTile / kBlock;
+constexpr int kThreads = 448;            // 8 softmax warps, K copies, matrix, 4 V warps
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kVWarp = 10;
+constexpr int kKStages = 3, kScaleSlots = 4;
+constexpr int kRows = 128;               // rows of a tile of queries
+constexpr int kChunk = 512;              // requests of one round of the search
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTop = 6.f;              // x of the maximum when it was taken: 2^6
+constexpr float kSlack = 8.f;            // the maximum moves when a row passes it by this
+
+// Units of request r: groups of `per` query tokens, all KV heads alike.
+struct Req {
+  int first, n, p0;      // first packed row; tokens handled (0: none); position of the first
+};
+__device__ __forceinline__ Req req_of(const PagedAttend& a, int r) {
+  Req x;
+  x.first = r;
+  x.n = 1;
+  int n = 1;
+  if (a.row_start) {
+    x.first = __ldg(a.row_start + r);
+    n = __ldg(a.row_start + r + 1) - x.first;
+    x.n = x.first < 0 ? 0 : min(min(n, a.max_q_len), a.total_q - x.first);
+  }
+  x.p0 = min(max(__ldg(a.kv_len + r), 0), a.table_stride * kBlock) - n;
+  return x;
+}
+struct Unit {
+  int i0, cnt;           // first query token of the request, tokens
+  int b0, nb, tiles;     // blocks that any of them sees
+};
+__device__ __forceinline__ Unit unit_of(const PagedAttend& a, const Req& x, int qg, int per) {
+  Unit u;
+  u.i0 = qg * per;
+  u.cnt = min(per, x.n - u.i0);
+  const int hi = max(x.p0 + u.i0 + u.cnt, 0);
+  const int lo = a.window > 0 ? max(x.p0 + u.i0 + 1 - a.window, 0) : 0;
+  u.b0 = lo / kBlock;
+  u.nb = max((hi + kBlock - 1) / kBlock - u.b0, 0);
+  u.tiles = max((u.nb + kTileBlocks - 1) / kTileBlocks, 1);
+  return u;
+}
+
+struct Search {
+  long long sums[32];
+  long long total, before;
+  int tiles[kChunk];
+  int r, qg, h, t;
+};
+
+// Tiles of request r per KV head, by a warp.
+__device__ int request_tiles(const PagedAttend& a, int r, int per) {
+  const Req x = req_of(a, r);
+  int sum = 0;
+  for (int qg = threadIdx.x & 31; qg * per < x.n; qg += 32) sum += unit_of(a, x, qg, per).tiles;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// Total tiles of the call, by a block of `warps` warps.
+__device__ long long total_tiles(const PagedAttend& a, int per, int warps, Search& s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long sum = 0;
+  for (int r = warp; r < a.n_reqs; r += warps) {
+    const int t = request_tiles(a, r, per);
+    if (lane == 0 && r < kChunk) s.tiles[r] = t;
+    sum += t;
+  }
+  if (lane == 0) s.sums[warp] = sum;
+  __syncthreads();
+  sum = 0;
+  for (int w = 0; w < warps; ++w) sum += s.sums[w];
+  return sum * a.d.Hkv;
+}
+
+// Where tile `target` of the call is: s.r, s.qg, s.h, s.t (tile within the unit), for all
+// threads.  After total_tiles, which left the first kChunk requests' counts.
+__device__ void locate(const PagedAttend& a, int per, int warps, long long target, Search& s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hkv = a.d.Hkv;
+  long long base = 0;
+  for (int r0 = 0; r0 < a.n_reqs; r0 += kChunk) {
+    const int m = min(kChunk, a.n_reqs - r0);
+    if (r0 > 0) {
+      __syncthreads();
+      for (int i = warp; i < m; i += warps) {
+        const int t = request_tiles(a, r0 + i, per);
+        if (lane == 0) s.tiles[i] = t;
+      }
+    }
+    if (threadIdx.x == 0) s.r = -1;
+    __syncthreads();
+    if (warp == 0) {
+      long long at = base;
+      for (int i = 0; i < m; i += 32) {
+        const long long mine = i + lane < m ? (long long)s.tiles[i + lane] * hkv : 0;
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+        upto += at;
+        if (target >= upto - mine && target < upto) {
+          s.r = r0 + i + lane;
+          s.before = upto - mine;
+        }
+        at = __shfl_sync(0xffffffffu, upto, 31);
+      }
+      if (lane == 0) s.total = at;
+    }
+    __syncthreads();
+    base = s.total;
+    if (s.r >= 0) break;
+  }
+  if (warp == 0) {
+    const Req x = req_of(a, s.r);
+    long long at = s.before;
+    for (int q0 = 0; q0 * per < x.n; q0 += 32) {
+      const int qg = q0 + lane;
+      const int tiles = qg * per < x.n ? unit_of(a, x, qg, per).tiles : 0;
+      const long long mine = (long long)tiles * hkv;
+      long long upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      upto += at;
+      if (target >= upto - mine && target < upto) {
+        const int off = (int)(target - (upto - mine));
+        s.qg = qg;
+        s.h = off / tiles;
+        s.t = off % tiles;
+      }
+      at = __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// A CTA's walk over its tiles, segment by segment (a segment: tiles of one unit).
+struct Walk {
+  int r, qg, h, t0, nt, left, per;
+  Req q;
+  Unit u;
+  bool first, whole;
+  __device__ void start(const PagedAttend& a, const Search& s, int tiles, int per_) {
+    r = s.r; qg = s.qg; h = s.h; t0 = s.t;
+    left = tiles;
+    per = per_;
+    first = true;
+    q = req_of(a, r);
+    u = unit_of(a, q, qg, per);
+    clip();
+  }
+  __device__ void clip() {
+    nt = min(u.tiles - t0, left);
+    whole = nt == u.tiles;
+  }
+  __device__ void next(const PagedAttend& a) {
+    left -= nt;
+    first = false;
+    t0 = 0;
+    if (left <= 0) return;
+    if (++h == a.d.Hkv) {
+      h = 0;
+      ++qg;
+      while (qg * per >= q.n) {
+        qg = 0;
+        q = req_of(a, ++r);
+      }
+      u = unit_of(a, q, qg, per);
+    }
+    clip();
+  }
+};
+
+struct Misc {
+  uint64_t k_full[kKStages], k_empty[kKStages], v_full, v_empty, drain;
+  uint64_t s_ready[2], p_ready[2], pv_done[2], q_ready[2];
+  uint32_t tmem;
+  float ks[kScaleSlots][kTileBlocks], ev[kScaleSlots][kTileBlocks], iv[kScaleSlots][kTileBlocks];
+  int bad[kScaleSlots];                    // blocks of the tile that are not a page, as bits
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int PAGE = 16 * D;
+  static constexpr int Q = kRows * 2 * D;                 // one tile of queries, both pieces
+  static constexpr int K = kTileBlocks * PAGE;            // a stage of K
+  static constexpr int V = kTile * D * 2;                 // V as f16
+  static constexpr int P = kRows * kTile * 2;             // one tile's probabilities
+  static constexpr int BODY = 2 * Q + 2 * P + kKStages * K + V;
+  static constexpr int SMEM = BODY + (int)sizeof(Misc) + 1024;
+  static_assert(SMEM + (int)sizeof(Search) <= 227 * 1024, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a, const int qpt) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Search search;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* sq = smem;
+  uint8_t* sp = sq + 2 * C::Q;
+  uint8_t* sk = sp + 2 * C::P;
+  uint8_t* sv = sk + kKStages * C::K;
+  Misc& ms = *reinterpret_cast<Misc*>(sv + C::V);
+  const PagedDev& d = a.d;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = 2 * qpt;                                // query tokens of a unit
+
+  launch_dependents();
+  if (blockIdx.x == 0) report_rows(a, kThreads);
+  const long long total = total_tiles(a, per, kThreads / 32, search);
+  const long long ctas = min((long long)gridDim.x, total);
+  if (blockIdx.x >= ctas) return;
+  const long long begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+  locate(a, per, kThreads / 32, begin, search);
+
+  if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(smem_u32(&ms.k_full[i]), 1);
+      mbar_init(smem_u32(&ms.k_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ms.v_full), 4);
+    mbar_init(smem_u32(&ms.v_empty), 1);
+    mbar_init(smem_u32(&ms.drain), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ms.s_ready[i]), 1);
+      mbar_init(smem_u32(&ms.p_ready[i]), 4);
+      mbar_init(smem_u32(&ms.pv_done[i]), 1);
+      mbar_init(smem_u32(&ms.q_ready[i]), 4);
+    }
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) {
+    umma::alloc(smem_u32(&ms.tmem), 512);
+    umma::relinquish();
+  }
+  umma::fence_before();
+  __syncthreads();
+  umma::fence_after();
+  const uint32_t tmem = ms.tmem;                          // S of A, S of B, O of A, O of B
+  Walk w;
+  w.start(a, search, (int)(end - begin), per);
+
+  if (warp == kCopyWarp) {
+    // ---- K pages and the blocks' scales: lane j < 8 has block j of the tile
+    const uint8_t* kbase = d.k + a.layer * d.layer_bytes;
+    const float2* sbase = d.scales + a.layer * d.layer_scales;
+    int count = 0;
+    bool ok = true;
+    while (w.left > 0 && ok) {
+      const int32_t* row = a.table + (size_t)w.r * a.table_stride;
+      auto fetch = [&](int t, int& nb, int& page, float2& sc) {
+        const int b = w.u.b0 + t * kTileBlocks;
+        nb = max(0, min(kTileBlocks, w.u.b0 + w.u.nb - b));
+        page = -1;
+        sc = make_float2(1.f, 1.f);
+        if (lane < nb) {
+          page = __ldg(row + b + lane);
+          if (page < 0 || page >= d.num_pages) {
+            paged_error(d, kErrState);
+            page = -1;
+          } else {
+            sc = __ldg(sbase + (size_t)page * d.Hkv + w.h);
+            sc.x = fmaxf(sc.x, exp2_int(kScaleMinExp));
+            sc.y = fmaxf(sc.y, exp2_int(kScaleMinExp));
+          }
+        }
+      };
+      int nb, page;
+      float2 sc;
+      fetch(w.t0, nb, page, sc);
+      for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
+        const int st = count % kKStages, slot = count % kScaleSlots;
+        if (count >= kKStages) ok = mbar_wait(smem_u32(&ms.k_empty[st]), (count / kKStages - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t full = smem_u32(&ms.k_full[st]), dst = smem_u32(sk + st * C::K);
+        const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
+        if (lane == 0) mbar_expect(full, __popc(good) * C::PAGE);
+        __syncwarp();
+        if (page >= 0) bulk_load(dst + lane * C::PAGE, kbase + ((size_t)page * d.Hkv + w.h) * C::PAGE, C::PAGE, full);
+        if (lane < kTileBlocks) {
+          const float ev = (float)((__float_as_int(sc.y) >> 23) - 127);
+          ms.ks[slot][lane] = sc.x;
+          ms.ev[slot][lane] = ev;
+          ms.iv[slot][lane] = exp2_int(-(int)ev);
+        }
+        if (lane == 0) ms.bad[slot] = (int)(~good & 0xffu);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+        if (t + 1 < w.t0 + w.nt) fetch(t + 1, nb, page, sc);
+      }
+      if (ok) w.next(a);
+    }
+    if (!ok && lane == 0) paged_error(d, kErrTimeout);
+    for (int i = max(0, count - kKStages); i < count; ++i) mbar_wait(smem_u32(&ms.k_full[i % kKStages]), (i / kKStages) & 1);
+  } else if (warp >= kVWarp) {
+    // ---- V: a page's row d (16 tokens of a dimension) becomes two 16-byte operand rows
+    constexpr int PPI = 128 / D;                          // pages of one pass of the 128 threads
+    constexpr int NI = kTileBlocks / PPI;
+    const int vt = tid - kVWarp * 32, dim = vt % D, pp = vt / D;
+    const uint8_t* vbase = d.v + a.layer * d.layer_bytes;
+    int count = 0;
+    bool ok = true;
+    uint4 raw[NI];
+    auto fetch = [&](const Walk& x, int t) {
+      const int b = x.u.b0 + t * kTileBlocks;
+      const int32_t* row = a.table + (size_t)x.r * a.table_stride;
+      int page[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int j = i * PPI + pp;
+        page[i] = b + j < x.u.b0 + x.u.nb ? __ldg(row + b + j) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        raw[i] = page[i] >= 0 && page[i] < d.num_pages
+                     ? __ldg(reinterpret_cast<const uint4*>(vbase + ((size_t)page[i] * d.Hkv + x.h) * C::PAGE + dim * 16))
+                     : make_uint4(0, 0, 0, 0);
+    };
+    fetch(w, w.t0);
+    while (w.left > 0 && ok) {
+      Walk x = w;
+      x.next(a);
+      for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
+        if (count > 0) ok = mbar_wait(smem_u32(&ms.v_empty), (count - 1) & 1);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const uint32_t* c = &raw[i].x;
+          uint32_t h[8];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * u]) : "h"((uint16_t)(c[u] & 0xffffu)));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * u + 1]) : "h"((uint16_t)(c[u] >> 16)));
+          }
+          uint4* dst = reinterpret_cast<uint4*>(sv + (size_t)(2 * (i * PPI + pp)) * (D * 16) + dim * 16);
+          dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+          dst[D] = make_uint4(h[4], h[5], h[6], h[7]);    // the next 8 tokens
+        }
+        umma::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms.v_full));
+        if (t + 1 < w.t0 + w.nt) fetch(w, t + 1);
+        else if (x.left > 0) fetch(x, x.t0);
+      }
+      w = x;
+    }
+    if (!ok && lane == 0) paged_error(d, kErrTimeout);
+  } else if (warp == kMmaWarp) {
+    // ---- matrix instructions, by one thread
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_e4m3(128, 128), id_pv = umma::idesc_f16(false, 128, D);
+      int count = 0, seg = 0, count_b = 0, seg_b = 0;
+      bool ok = true;
+      auto qk = [&](int x, int n) {                       // S of tile x from K number n
+        const uint32_t aq = smem_u32(sq + x * C::Q), bk = smem_u32(sk + (n % kKStages) * C::K);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)                  // the pieces hi, then lo, over the same K
+          mma_e4m3(tmem + x * 128, desc(aq + k * 2 * kRows * 16, kRows * 16, 128),
+                   desc(bk + (k % (D / 32)) * 256, 128, 8 * D), id_qk, k > 0);
+        umma::commit(smem_u32(&ms.s_ready[x]));
+      };
+      auto pv = [&](int x, bool fresh) {
+        const uint32_t ap = smem_u32(sp + x * C::P), bv = smem_u32(sv);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma::mma_f16(tmem + 256 + x * 128, desc(ap + k * 2 * kRows * 16, kRows * 16, 128),
+                        desc(bv + k * 2 * D * 16, D * 16, 128), id_pv, !(fresh && k == 0));
+        umma::commit(smem_u32(&ms.pv_done[x]));
+      };
+      while (w.left > 0 && ok) {
+        const bool two = w.u.cnt > qpt;
+        ok = mbar_wait(smem_u32(&ms.q_ready[0]), seg & 1);
+        if (ok && two) ok = mbar_wait(smem_u32(&ms.q_ready[1]), seg_b & 1);
+        if (ok) ok = mbar_wait(smem_u32(&ms.k_full[count % kKStages]), (count / kKStages) & 1);
+        if (!ok) break;
+        umma::fence_after();
+        qk(0, count);
+        if (two) qk(1, count);
+        umma::commit(smem_u32(&ms.k_empty[count % kKStages]));
+        for (int t = 0; t < w.nt && ok; ++t, ++count) {
+          const bool more = t + 1 < w.nt;
+          const int n = count + 1;
+          if (more) ok = mbar_wait(smem_u32(&ms.k_full[n % kKStages]), (n / kKStages) & 1);
+          if (ok) ok = mbar_wait(smem_u32(&ms.p_ready[0]), count & 1);
+          if (!ok) break;
+          umma::fence_after();
+          if (more) qk(0, n);
+          ok = mbar_wait(smem_u32(&ms.v_full), count & 1);
+          if (!ok) break;
+          umma::fence_after();
+          pv(0, t == 0);
+          if (two) {
+            ok = mbar_wait(smem_u32(&ms.p_ready[1]), count_b & 1);
+            if (!ok) break;
+            ++count_b;
+            umma::fence_after();
+            if (more) qk(1, n);
+          }
+          if (more) umma::commit(smem_u32(&ms.k_empty[n % kKStages]));
+          if (two) pv(1, t == 0);
+          umma::commit(smem_u32(&ms.v_empty));
+        }
+        if (!ok) break;
+        ++seg;
+        if (two) ++seg_b;
+        w.next(a);
+      }
+      if (!ok) paged_error(d, kErrTimeout);
+      umma::commit(smem_u32(&ms.drain));
+      mbar_wait(smem_u32(&ms.drain), 0);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax of tile x: a thread to a row
+    const int x = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + x * 128 + lanes, t_o = tmem + 256 + x * 128 + lanes;
+    const int token = row / d.G, head = row % d.G;        // of the tile
+    const float qk = kLog2e * rsqrtf((float)D);
+    uint8_t* q_at = sq + x * C::Q + row * 16;
+    uint8_t* p_at = sp + x * C::P + row * 16;
+    int count = 0;
+    bool ok = true;
+    float c = 0.f;
+    // the row's query in two pieces, chunk by chunk of 16 dimensions
+    auto load_q = [&](const Walk& y) {
+      const int i = x * qpt + token;
+      const bool live = token < qpt && i < y.u.cnt;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+          (live ? ((size_t)(y.q.first + y.u.i0 + i) * d.Hq + y.h * d.G + head) * D : 0));
+      float amax = 0.f;
+#pragma unroll 4
+      for (int j = 0; j < D / 8; ++j) {
+        const uint4 v = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 f = __bfloat1622float2(p[u]);
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      const int e = scale_exp(amax);
+      const float up = exp2_int(-e);
+      c = exp2_int(live ? e : 0) * qk;
+#pragma unroll 2
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint4 v = live ? __ldg(src + 2 * j + k) : make_uint4(0, 0, 0, 0);
+          const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float2 f = __bfloat1622float2(p[2 * u]), g = __bfloat1622float2(p[2 * u + 1]);
+            const uint32_t h0 = float2_to_e4m3x2(f.x * up, f.y * up), h1 = float2_to_e4m3x2(g.x * up, g.y * up);
+            const float2 b0 = e4m3x2_to_float2(h0), b1 = e4m3x2_to_float2(h1);
+            hi[2 * k + u] = h0 | h1 << 16;
+            lo[2 * k + u] = float2_to_e4m3x2(f.x * up - b0.x, f.y * up - b0.y) |
+                            float2_to_e4m3x2(g.x * up - b1.x, g.y * up - b1.y) << 16;
+          }
+        }
+        *reinterpret_cast<uint4*>(q_at + (size_t)j * (kRows * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(q_at + (size_t)(j + D / 16) * (kRows * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      umma::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready[x]));
+    };
+    auto mine = [&](const Walk& y) { return x == 0 || y.u.cnt > qpt; };
+    // the first segment that has this tile, and its place in the scale slots
+    int tile = 0;                                         // tiles of the CTA before the segment
+    while (w.left > 0 && !mine(w)) { tile += w.nt; w.next(a); }
+    if (w.left > 0) load_q(w);
+    while (w.left > 0 && ok) {
+      float m = -INFINITY, l = 0.f;
+      const int i = x * qpt + token;                      // the row's token of the unit
+      const bool live = token < qpt && i < w.u.cnt;
+      const int hi = w.q.p0 + w.u.i0 + i + 1, lo = a.window > 0 ? hi - a.window : 0;
+      // positions that all live rows of the tile see
+      const int all_hi = w.q.p0 + w.u.i0 + x * qpt + 1;
+      const int last = w.q.p0 + w.u.i0 + min(w.u.cnt, (x + 1) * qpt);
+      const int all_lo = a.window > 0 ? max(last - a.window, 0) : 0;
+      for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
+        const int slot = (tile + t - w.t0) % kScaleSlots;
+        ok = mbar_wait(smem_u32(&ms.s_ready[x]), count & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        umma::fence_after();
+        const int base = (w.u.b0 + t * kTileBlocks) * kBlock;
+        const int bad = ms.bad[slot];
+        const bool masked = base < all_lo || base + kTile > all_hi || bad;
+        // the row's maximum, from each block's largest product
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float s[32];
+          umma::ld32(t_s + 32 * j, s);
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const int pos = base + 32 * j + k;
+              if (pos >= hi || pos < lo || (bad >> (2 * j + k / 16) & 1)) s[k] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float v = s[16 * b];
+#pragma unroll
+            for (int k = 1; k < 16; ++k) v = fmaxf(v, s[16 * b + k]);
+            const float tb = fmaf(v, ms.ks[slot][2 * j + b] * c, ms.ev[slot][2 * j + b]);
+            top = fmaxf(top, v == -INFINITY ? -INFINITY : tb);
+          }
+        }
+        float f = 1.f;
+        if (top > m + kSlack || (m == -INFINITY && top > -INFINITY)) {
+          f = ex2(m - top);                               // 0 the first time
+          m = top;
+        }
+        const float ref = (m == -INFINITY ? 0.f : m) - kTop;
+        // the previous product is done with the probabilities' buffer and the output
+        if (t > w.t0) {
+          ok = mbar_wait(smem_u32(&ms.pv_done[x]), (count - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          umma::fence_after();
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+            for (int j = 0; j < D; j += 16) {
+              float o[16];
+              ld16(t_o + j, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= f;
+              st16(t_o + j, o);
+            }
+            wait_st();
+          }
+        }
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float s[32];
+          umma::ld32(t_s + 32 * j, s);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float mul = ms.ks[slot][2 * j + b] * c, sub = ms.ev[slot][2 * j + b] - ref;
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float v = ex2(fmaf(s[16 * b + k], mul, sub));
+              if (masked) {
+                const int pos = base + 32 * j + 16 * b + k;
+                if (pos >= hi || pos < lo || (bad >> (2 * j + b) & 1)) v = 0.f;
+              }
+              s[16 * b + k] = v;
+              sum += v;
+            }
+            l = fmaf(sum, ms.iv[slot][2 * j + b], l);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {                   // 8 tokens to a 16-byte operand row
+            uint32_t h[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const __half2 y = __floats2half2_rn(s[8 * k + 2 * u], s[8 * k + 2 * u + 1]);
+              h[u] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            *reinterpret_cast<uint4*>(p_at + (size_t)(4 * j + k) * (kRows * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        umma::fence_async_smem();
+        umma::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready[x]));
+      }
+      if (!ok) break;
+      // the next segment's queries while the last product runs
+      const Walk y = w;
+      tile += w.nt;
+      w.next(a);
+      while (w.left > 0 && !mine(w)) { tile += w.nt; w.next(a); }
+      if (w.left > 0) load_q(w);
+      ok = mbar_wait(smem_u32(&ms.pv_done[x]), (count - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      umma::fence_after();
+      if (y.whole) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+            (live ? ((size_t)(y.q.first + y.u.i0 + i) * d.Hq + y.h * d.G + head) * D : 0);
+#pragma unroll
+        for (int j = 0; j < D; j += 16) {
+          float o[16];
+          ld16(t_o + j, o);
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+            h[k] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          if (live) {
+            reinterpret_cast<uint4*>(out + j)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            reinterpret_cast<uint4*>(out + j)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+        }
+      } else {
+        const size_t rec = ((size_t)(2 * blockIdx.x + (y.first ? 0 : 1)) * 2 + x) * kRows + row;
+#pragma unroll
+        for (int j = 0; j < D; j += 16) {
+          float o[16];
+          ld16(t_o + j, o);
+          if (live) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + rec * D + j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        }
+        if (live) a.part_ml[rec] = make_float2(m, l);
+      }
+      umma::fence_before();
+    }
+    if (!ok && lane == 0) paged_error(d, kErrTimeout);
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    umma::fence_after();
+    umma::dealloc(tmem, 512);
+  }
+}
+
+// Adds the partials of the unit that CTA boundary blockIdx.x + 1 cuts, if that is the unit's first cut.
+constexpr int kJoinThreads = 128, kJoinRows = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAttend a, const int qpt,
+                                                                   const int grid) {
+  __shared__ Search search;
+  const PagedDev& d = a.d;
+  const int per = 2 * qpt, c = blockIdx.x + 1;
+  const long long total = total_tiles(a, per, kJoinThreads / 32, search);
+  const int ctas = (int)min((long long)grid, total);
+  bool work = c < ctas;
+  long long off = 0;
+  if (work) {
+    const long long begin = total * c / ctas;
+    locate(a, per, kJoinThreads / 32, begin, search);
+    off = begin - search.t;                               // the unit's first tile
+    work = search.t > 0 && total * (c - 1) / ctas <= off;
+  }
+  wait_previous();
+  if (!work) return;
+  const Req q = req_of(a, search.r);
+  const Unit u = unit_of(a, q, search.qg, per);
+  const int c0 = c - 1;
+  int c1 = c;
+  while (c1 + 1 < ctas && total * (c1 + 1) / ctas < off + u.tiles) ++c1;
+  for (int k = 0; k < kJoinRows; ++k) {
+    const int pr = blockIdx.y * kJoinRows + k, x = pr / kRows, row = pr % kRows;   // of the unit's 256 rows
+    const int i = x * qpt + row / d.G;
+    if (row / d.G >= qpt || i >= u.cnt) continue;
+    auto rec_of = [&](int e) {
+      const bool first = off <= total * e / ctas;         // the unit is the CTA's first
+      return ((size_t)(2 * e + (first ? 0 : 1)) * 2 + x) * kRows + row;
+    };
+    float top = -INFINITY;
+    for (int e = c0; e <= c1; ++e) top = fmaxf(top, a.part_ml[rec_of(e)].x);
+    const float ref = top > -INFINITY ? top : 0.f;
+    float sum = 0.f, acc = 0.f;
+#pragma unroll 4
+    for (int e = c0; e <= c1; ++e) {
+      const size_t rec = rec_of(e);
+      const float2 ml = a.part_ml[rec];
+      const float f = ex2(ml.x - ref);
+      sum = fmaf(ml.y, f, sum);
+      if (threadIdx.x < D) acc = fmaf(a.part_o[rec * D + threadIdx.x], f, acc);
+    }
+    if (threadIdx.x < D)
+      static_cast<__nv_bfloat16*>(a.out)[((size_t)(q.first + u.i0 + i) * d.Hq + search.h * d.G + row % d.G) * D + threadIdx.x] =
+          __float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const PagedAttend& a, int grid, cudaStream_t st) {
+  using C = Cfg<D>;
+  static std::atomic<unsigned long long> opted{0};
+  cudaError_t e = smem_optin_once(opted, prompt_kernel<D>, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int qpt = kRows / a.d.G;
+  prompt_kernel<D><<<grid, kThreads, C::SMEM, st>>>(a, qpt);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || grid == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid - 1, 2 * kRows / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D>, a, qpt, grid);
+}
+
+}  // namespace
+
+int paged_prompt_rows() { return 2 * kRows; }
+
+cudaError_t launch_paged_prompt(const PagedAttend& a, int grid, cudaStream_t st) {
+  return a.d.D == 64 ? launch_d<64>(a, grid, st) : launch_d<128>(a, grid, st);
+}
+
+}  // namespace kvs
