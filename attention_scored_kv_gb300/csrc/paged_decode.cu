@@ -20,8 +20,7 @@
 // How: the 128-token tiles of all units are laid end to end and cut evenly over a
 // persistent grid, two CTAs to an SM (each CTA finds its range from the device lengths by
 // itself); a unit that a cut splits leaves float32 partials which the join kernel adds.
-// Per CTA one warp issues the pages' bulk copies into a ring, one thread the matrix
-// instructions, four warps the softmax (a thread is a token, so scales and masks are one
+// Per CTA one warp issues the pages' bulk copies into a ring, one the matrix instructions, four warps the softmax (a thread is a token, so scales and masks are one
 // per thread and the probabilities go to shared memory as bytes).  S is double buffered:
 // the next tile's S is computed under this one's softmax.
 #include "paged_mma.cuh"
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
   uint8_t* sp = sq + 2 * C::Q;
   Misc& ms = *reinterpret_cast<Misc*>(sp + C::P);
   const PagedDev& d = a.d;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   launch_dependents();
   if (blockIdx.x == 0) report_rows(a, kThreads);
@@ -295,54 +294,53 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
     // copies still in flight land before the CTA ends
     for (int i = max(0, count - C::NS); i < count; ++i) mbar_wait(smem_u32(&ms.full[i % C::NS]), (i / C::NS) & 1);
   } else if (warp == 5) {
-    // ---- matrix instructions, by one thread
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_e4m3(128, N);
-      int count = 0, seg = 0;
-      bool ok = true;
-      auto pv = [&](int i, int nb, bool fresh) {            // tile number i of the CTA
-        const int st = i % C::NS;
-        umma::fence_after();
-        const uint32_t av = smem_u32(ring + st * C::STAGE + C::HALF), bp = smem_u32(sp);
-        const int steps = (nb + 1) / 2;
-        for (int k = 0; k < steps; ++k)
-          mma_e4m3(t_o, desc(av + k * 2 * C::PAGE, C::PAGE, 128), desc(bp + k * 2 * N * 16, N * 16, 128), id,
-                   !(fresh && k == 0));
-        umma::commit(smem_u32(&ms.empty[st]));
-        umma::commit(smem_u32(&ms.o_done));
-      };
-      while (w.left > 0 && ok) {
-        ok = mbar_wait(smem_u32(&ms.q_ready), seg & 1);
-        const uint32_t bq = smem_u32(sq + (seg & 1) * C::Q);
-        int nb_before = 0;
-        for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
-          const int st = count % C::NS, nb = max(0, min(kTileBlocks, w.u.nb - t * kTileBlocks));
-          ok = mbar_wait(smem_u32(&ms.full[st]), (count / C::NS) & 1);
-          if (!ok) break;
-          umma::fence_after();
-          const uint32_t ak = smem_u32(ring + st * C::STAGE);
+    // ---- matrix instructions
+    constexpr uint32_t id = idesc_e4m3(128, N);
+    const uint32_t on = elect();
+    int count = 0, seg = 0;
+    bool ok = true;
+    auto pv = [&](int i, int nb, bool fresh) {              // tile number i of the CTA
+      const int st = i % C::NS, steps = (nb + 1) / 2;
+      umma::fence_after();
+      const uint32_t av = desc_lo(smem_u32(ring + st * C::STAGE + C::HALF), C::PAGE), bp = desc_lo(smem_u32(sp), N * 16);
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            mma_e4m3(tmem + (count & 1) * N, desc(ak + k * 256, 128, 8 * D), desc(bq + k * 256, 128, 8 * D), id, k > 0);
-          umma::commit(smem_u32(&ms.s_ready[count & 1]));
-          if (t > w.t0) {
-            ok = mbar_wait(smem_u32(&ms.p_ready), (count - 1) & 1);
-            if (!ok) break;
-            pv(count - 1, nb_before, t - 1 == w.t0);
-          }
-          nb_before = nb;
-        }
-        if (ok) ok = mbar_wait(smem_u32(&ms.p_ready), (count - 1) & 1);
+      for (int k = 0; k < kTileBlocks / 2; ++k)
+        if (k < steps)
+          mma_e4m3(on, t_o, av + k * (2 * C::PAGE / 16), desc_hi(128), bp + k * (2 * N), desc_hi(128), id,
+                   !(fresh && k == 0));
+      commit(on, smem_u32(&ms.empty[st]));
+      commit(on, smem_u32(&ms.o_done));
+    };
+    while (w.left > 0 && ok) {
+      ok = warp_wait(smem_u32(&ms.q_ready), seg & 1);
+      const uint32_t bq = desc_lo(smem_u32(sq + (seg & 1) * C::Q), 128);
+      int nb_before = 0;
+      for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
+        const int st = count % C::NS, nb = max(0, min(kTileBlocks, w.u.nb - t * kTileBlocks));
+        ok = warp_wait(smem_u32(&ms.full[st]), (count / C::NS) & 1);
         if (!ok) break;
-        pv(count - 1, nb_before, w.nt == 1);
-        ++seg;
-        w.next(a);
+        umma::fence_after();
+        const uint32_t ak = desc_lo(smem_u32(ring + st * C::STAGE), 128);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          mma_e4m3(on, tmem + (count & 1) * N, ak + k * 16, desc_hi(8 * D), bq + k * 16, desc_hi(8 * D), id, k > 0);
+        commit(on, smem_u32(&ms.s_ready[count & 1]));
+        if (t > w.t0) {
+          ok = warp_wait(smem_u32(&ms.p_ready), (count - 1) & 1);
+          if (!ok) break;
+          pv(count - 1, nb_before, t - 1 == w.t0);
+        }
+        nb_before = nb;
       }
-      if (!ok) paged_error(d, kErrTimeout);
-      umma::commit(smem_u32(&ms.drain));
-      mbar_wait(smem_u32(&ms.drain), 0);
+      if (ok) ok = warp_wait(smem_u32(&ms.p_ready), (count - 1) & 1);
+      if (!ok) break;
+      pv(count - 1, nb_before, w.nt == 1);
+      ++seg;
+      w.next(a);
     }
-    __syncwarp();
+    if (!ok && lane == 0) paged_error(d, kErrTimeout);
+    commit(on, smem_u32(&ms.drain));
+    mbar_wait(smem_u32(&ms.drain), 0);
   } else {
     // ---- softmax: thread = token of the tile, then = dimension of the output
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;

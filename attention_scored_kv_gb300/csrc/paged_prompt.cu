@@ -20,8 +20,10 @@
 // rows (a page's rows are its operand rows, so it is load, convert, store), one thread
 // issues the matrix instructions, and two groups of four warps do the softmax of A and B, a
 // thread to a row, so that no row statistic crosses threads.  The matrix thread works on
-// one tile while the other's softmax runs: S(A, j+1) and O(A) += X(A, j) V while B's
-// exponentials are computed, then the reverse.
+// one tile while the other's softmax runs: O(A) += X(A, j) V and S(A, j+1) while B's
+// exponentials are computed, then the reverse.  X goes to TMEM, over S, as the product's
+// first operand: from shared memory the two operands of both products, X's stores and V's
+// would be 368 KB a step, 2900 clocks at 128 bytes, against the tensor core's 2048.
 #include "paged_mma.cuh"
 
 namespace kvs {
@@ -30,14 +32,15 @@ namespace {
 using namespace pmma;
 
 constexpr int kTile = 128, kTileBlocks = kTile / kBlock;
-constexpr int kThreads = 448;            // 8 softmax warps, K copies, matrix, 4 V warps
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kVWarp = 10;
-constexpr int kKStages = 3, kScaleSlots = 4;
+constexpr int kThreads = 384;            // 8 softmax warps, K copies, matrix, 2 V warps
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kVWarp = 10, kVThreads = 64;
+constexpr int kKStages = 3, kVStages = 2, kScaleSlots = 4;
 constexpr int kRows = 128;               // rows of a tile of queries
 constexpr int kChunk = 512;              // requests of one round of the search
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTop = 6.f;              // x of the maximum when it was taken: 2^6
 constexpr float kSlack = 8.f;            // the maximum moves when a row passes it by this
+constexpr float kLimit = 16384.f;        // 2^(kTop + kSlack): more in a block's sum, and the maximum is looked at
 
 // Units of request r: groups of `per` query tokens, all KV heads alike.
 struct Req {
@@ -208,10 +211,10 @@ struct Walk {
 };
 
 struct Misc {
-  uint64_t k_full[kKStages], k_empty[kKStages], v_full, v_empty, drain;
-  uint64_t s_ready[2], p_ready[2], pv_done[2], q_ready[2];
+  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], drain;
+  uint64_t s_ready[2], p_ready[2], o_done[2], q_ready[2];
   uint32_t tmem;
-  float ks[kScaleSlots][kTileBlocks], ev[kScaleSlots][kTileBlocks], iv[kScaleSlots][kTileBlocks];
+  alignas(16) float ks[kScaleSlots][kTileBlocks], vs[kScaleSlots][kTileBlocks];
   int bad[kScaleSlots];                    // blocks of the tile that are not a page, as bits
 };
 
@@ -221,11 +224,86 @@ struct Cfg {
   static constexpr int Q = kRows * 2 * D;                 // one tile of queries, both pieces
   static constexpr int K = kTileBlocks * PAGE;            // a stage of K
   static constexpr int V = kTile * D * 2;                 // V as f16
-  static constexpr int P = kRows * kTile * 2;             // one tile's probabilities
-  static constexpr int BODY = 2 * Q + 2 * P + kKStages * K + V;
+  static constexpr int BODY = 2 * Q + kKStages * K + kVStages * V;
   static constexpr int SMEM = BODY + (int)sizeof(Misc) + 1024;
   static_assert(SMEM + (int)sizeof(Search) <= 227 * 1024, "shared memory");
 };
+
+// What a row's thread needs of a tile of 128 tokens: the blocks' scales and what it sees.
+struct Tile {
+  float ks[kTileBlocks], vs[kTileBlocks];  // in registers: the operands' traffic starves shared-memory loads
+  int base, lo, hi;      // first position; the row sees [lo, hi)
+  uint32_t bad;          // blocks that are not a page
+  __device__ __forceinline__ bool hidden(int k) const {
+    return base + k >= hi || base + k < lo || (bad >> (k >> 4) & 1);
+  }
+  __device__ __forceinline__ float ev(int b) const { return (float)((__float_as_int(vs[b]) >> 23) - 127); }
+  __device__ __forceinline__ float iv(int b) const { return __int_as_float((254 << 23) - __float_as_int(vs[b])); }
+};
+
+// The largest t of the row's tokens.
+template <bool MASK>
+__device__ __forceinline__ float row_max(uint32_t t_s, const Tile& y, float c) {
+  float top = -INFINITY;
+  uint32_t r[2][16];
+  ld16_start(t_s, r[0]);
+#pragma unroll
+  for (int b = 0; b < kTileBlocks; ++b) {
+    ld16_wait(r[b & 1]);
+    if (b + 1 < kTileBlocks) ld16_start(t_s + 16 * (b + 1), r[(b + 1) & 1]);
+    float s[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      s[k] = __uint_as_float(r[b & 1][k]);
+      if (MASK && y.hidden(16 * b + k)) s[k] = -INFINITY;
+    }
+    float v = max3(s[0], s[1], s[2]), u = max3(s[3], s[4], s[5]);
+    v = max3(v, s[6], s[7]);
+    u = max3(u, s[8], s[9]);
+    v = max3(v, s[10], s[11]);
+    u = max3(u, s[12], s[13]);
+    v = max3(v, s[14], s[15]);
+    v = fmaxf(v, u);
+    const float tb = fmaf(v, y.ks[b] * c, y.ev(b));
+    top = fmaxf(top, MASK && v == -INFINITY ? v : tb);
+  }
+  return top;
+}
+
+// x = 2^(t - ref) of the row's tokens as f16 pairs; the largest sum of a block to `big`.
+// Returns the row's part of l.
+template <bool MASK>
+__device__ __forceinline__ float row_exp(uint32_t t_s, const Tile& y, float c, float ref, uint32_t (&h)[64], float& big) {
+  float l = 0.f;
+  big = 0.f;
+  uint32_t r[2][16];
+  ld16_start(t_s, r[0]);
+#pragma unroll
+  for (int b = 0; b < kTileBlocks; ++b) {
+    ld16_wait(r[b & 1]);
+    if (b + 1 < kTileBlocks) ld16_start(t_s + 16 * (b + 1), r[(b + 1) & 1]);
+    const float m1 = y.ks[b] * c, s1 = y.ev(b) - ref;
+    const uint64_t mul = pack2(m1, m1), sub = pack2(s1, s1);
+    uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 t = unpack2(fma2(pack2(__uint_as_float(r[b & 1][2 * k]), __uint_as_float(r[b & 1][2 * k + 1])), mul, sub));
+      float x0 = ex2(t.x), x1 = ex2(t.y);
+      if (MASK) {
+        if (y.hidden(16 * b + 2 * k)) x0 = 0.f;
+        if (y.hidden(16 * b + 2 * k + 1)) x1 = 0.f;
+      }
+      if (k & 1) sum1 = add2(sum1, pack2(x0, x1)); else sum0 = add2(sum0, pack2(x0, x1));
+      const __half2 p = __floats2half2_rn(x0, x1);
+      h[8 * b + k] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    const float2 f = unpack2(add2(sum0, sum1));
+    const float s = f.x + f.y;
+    big = fmaxf(big, s);
+    l = fmaf(s, y.iv(b), l);
+  }
+  return l;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a, const int qpt) {
@@ -234,12 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
   __shared__ Search search;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sq = smem;
-  uint8_t* sp = sq + 2 * C::Q;
-  uint8_t* sk = sp + 2 * C::P;
+  uint8_t* sk = sq + 2 * C::Q;
   uint8_t* sv = sk + kKStages * C::K;
-  Misc& ms = *reinterpret_cast<Misc*>(sv + C::V);
+  Misc& ms = *reinterpret_cast<Misc*>(sv + kVStages * C::V);
   const PagedDev& d = a.d;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int per = 2 * qpt;                                // query tokens of a unit
 
   launch_dependents();
@@ -255,13 +332,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       mbar_init(smem_u32(&ms.k_full[i]), 1);
       mbar_init(smem_u32(&ms.k_empty[i]), 1);
     }
-    mbar_init(smem_u32(&ms.v_full), 4);
-    mbar_init(smem_u32(&ms.v_empty), 1);
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(smem_u32(&ms.v_full[i]), kVThreads / 32);
+      mbar_init(smem_u32(&ms.v_empty[i]), 1);
+    }
     mbar_init(smem_u32(&ms.drain), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms.s_ready[i]), 1);
       mbar_init(smem_u32(&ms.p_ready[i]), 4);
-      mbar_init(smem_u32(&ms.pv_done[i]), 1);
+      mbar_init(smem_u32(&ms.o_done[i]), 1);
       mbar_init(smem_u32(&ms.q_ready[i]), 4);
     }
     mbar_fence_init();
@@ -316,10 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
         __syncwarp();
         if (page >= 0) bulk_load(dst + lane * C::PAGE, kbase + ((size_t)page * d.Hkv + w.h) * C::PAGE, C::PAGE, full);
         if (lane < kTileBlocks) {
-          const float ev = (float)((__float_as_int(sc.y) >> 23) - 127);
           ms.ks[slot][lane] = sc.x;
-          ms.ev[slot][lane] = ev;
-          ms.iv[slot][lane] = exp2_int(-(int)ev);
+          ms.vs[slot][lane] = sc.y;
         }
         if (lane == 0) ms.bad[slot] = (int)(~good & 0xffu);
         __syncwarp();
@@ -332,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
     for (int i = max(0, count - kKStages); i < count; ++i) mbar_wait(smem_u32(&ms.k_full[i % kKStages]), (i / kKStages) & 1);
   } else if (warp >= kVWarp) {
     // ---- V: a page's row d (16 tokens of a dimension) becomes two 16-byte operand rows
-    constexpr int PPI = 128 / D;                          // pages of one pass of the 128 threads
-    constexpr int NI = kTileBlocks / PPI;
-    const int vt = tid - kVWarp * 32, dim = vt % D, pp = vt / D;
+    constexpr int DPT = D / kVThreads;                    // dimensions of a thread
+    constexpr int NI = kTileBlocks * DPT;
+    const int vt = tid - kVWarp * 32;
     const uint8_t* vbase = d.v + a.layer * d.layer_bytes;
     int count = 0;
     bool ok = true;
@@ -342,24 +419,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
     auto fetch = [&](const Walk& x, int t) {
       const int b = x.u.b0 + t * kTileBlocks;
       const int32_t* row = a.table + (size_t)x.r * a.table_stride;
-      int page[NI];
+      int page[kTileBlocks];
+#pragma unroll
+      for (int j = 0; j < kTileBlocks; ++j) page[j] = b + j < x.u.b0 + x.u.nb ? __ldg(row + b + j) : -1;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int j = i * PPI + pp;
-        page[i] = b + j < x.u.b0 + x.u.nb ? __ldg(row + b + j) : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        raw[i] = page[i] >= 0 && page[i] < d.num_pages
-                     ? __ldg(reinterpret_cast<const uint4*>(vbase + ((size_t)page[i] * d.Hkv + x.h) * C::PAGE + dim * 16))
+        const int pg = page[i / DPT], dim = vt + (i % DPT) * kVThreads;
+        raw[i] = pg >= 0 && pg < d.num_pages
+                     ? __ldg(reinterpret_cast<const uint4*>(vbase + ((size_t)pg * d.Hkv + x.h) * C::PAGE + dim * 16))
                      : make_uint4(0, 0, 0, 0);
+      }
     };
     fetch(w, w.t0);
     while (w.left > 0 && ok) {
       Walk x = w;
       x.next(a);
       for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
-        if (count > 0) ok = mbar_wait(smem_u32(&ms.v_empty), (count - 1) & 1);
+        const int st = count % kVStages;
+        if (count >= kVStages) ok = warp_wait(smem_u32(&ms.v_empty[st]), (count / kVStages - 1) & 1);
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -370,13 +447,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * u]) : "h"((uint16_t)(c[u] & 0xffffu)));
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * u + 1]) : "h"((uint16_t)(c[u] >> 16)));
           }
-          uint4* dst = reinterpret_cast<uint4*>(sv + (size_t)(2 * (i * PPI + pp)) * (D * 16) + dim * 16);
+          uint4* dst = reinterpret_cast<uint4*>(sv + st * C::V + (size_t)(2 * (i / DPT)) * (D * 16) + (vt + (i % DPT) * kVThreads) * 16);
           dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
           dst[D] = make_uint4(h[4], h[5], h[6], h[7]);    // the next 8 tokens
         }
         umma::fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms.v_full));
+        if (lane == 0) mbar_arrive(smem_u32(&ms.v_full[st]));
         if (t + 1 < w.t0 + w.nt) fetch(w, t + 1);
         else if (x.left > 0) fetch(x, x.t0);
       }
@@ -384,70 +461,67 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
     }
     if (!ok && lane == 0) paged_error(d, kErrTimeout);
   } else if (warp == kMmaWarp) {
-    // ---- matrix instructions, by one thread
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_e4m3(128, 128), id_pv = umma::idesc_f16(false, 128, D);
-      int count = 0, seg = 0, count_b = 0, seg_b = 0;
-      bool ok = true;
-      auto qk = [&](int x, int n) {                       // S of tile x from K number n
-        const uint32_t aq = smem_u32(sq + x * C::Q), bk = smem_u32(sk + (n % kKStages) * C::K);
+    // ---- matrix instructions
+    constexpr uint32_t id_qk = idesc_e4m3(128, 128), id_pv = umma::idesc_f16(false, 128, D);
+    const uint32_t on = elect();
+    int count = 0, seg = 0, count_b = 0, seg_b = 0;
+    bool ok = true;
+    auto qk = [&](int x, int n) {                         // S of tile x from K number n
+      const uint32_t aq = desc_lo(smem_u32(sq + x * C::Q), kRows * 16);
+      const uint32_t bk = desc_lo(smem_u32(sk + (n % kKStages) * C::K), 128);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)                  // the pieces hi, then lo, over the same K
-          mma_e4m3(tmem + x * 128, desc(aq + k * 2 * kRows * 16, kRows * 16, 128),
-                   desc(bk + (k % (D / 32)) * 256, 128, 8 * D), id_qk, k > 0);
-        umma::commit(smem_u32(&ms.s_ready[x]));
-      };
-      auto pv = [&](int x, bool fresh) {
-        const uint32_t ap = smem_u32(sp + x * C::P), bv = smem_u32(sv);
+      for (int k = 0; k < D / 16; ++k)                    // the pieces hi, then lo, over the same K
+        mma_e4m3(on, tmem + x * 128, aq + k * (2 * kRows), desc_hi(128), bk + (k % (D / 32)) * 16, desc_hi(8 * D),
+                 id_qk, k > 0);
+      commit(on, smem_u32(&ms.s_ready[x]));
+    };
+    auto pv = [&](int x, int n, bool fresh, bool last) {  // O of tile x with V number n
+      const uint32_t bv = desc_lo(smem_u32(sv + (n % kVStages) * C::V), D * 16);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma::mma_f16(tmem + 256 + x * 128, desc(ap + k * 2 * kRows * 16, kRows * 16, 128),
-                        desc(bv + k * 2 * D * 16, D * 16, 128), id_pv, !(fresh && k == 0));
-        umma::commit(smem_u32(&ms.pv_done[x]));
-      };
-      while (w.left > 0 && ok) {
-        const bool two = w.u.cnt > qpt;
-        ok = mbar_wait(smem_u32(&ms.q_ready[0]), seg & 1);
-        if (ok && two) ok = mbar_wait(smem_u32(&ms.q_ready[1]), seg_b & 1);
-        if (ok) ok = mbar_wait(smem_u32(&ms.k_full[count % kKStages]), (count / kKStages) & 1);
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_f16_ts(on, tmem + 256 + x * 128, tmem + x * 128 + k * 8, bv + k * (2 * D), desc_hi(128), id_pv,
+                   !(fresh && k == 0));
+      if (last) commit(on, smem_u32(&ms.o_done[x]));
+    };
+    while (w.left > 0 && ok) {
+      const bool two = w.u.cnt > qpt;
+      ok = warp_wait(smem_u32(&ms.q_ready[0]), seg & 1);
+      if (two) ok = ok && warp_wait(smem_u32(&ms.q_ready[1]), seg_b & 1);
+      ok = ok && warp_wait(smem_u32(&ms.k_full[count % kKStages]), (count / kKStages) & 1);
+      if (!ok) break;
+      umma::fence_after();
+      qk(0, count);
+      if (two) qk(1, count);
+      commit(on, smem_u32(&ms.k_empty[count % kKStages]));
+      for (int t = 0; t < w.nt && ok; ++t, ++count) {
+        const bool more = t + 1 < w.nt;
+        const int n = count + 1;
+        ok = warp_wait(smem_u32(&ms.v_full[count % kVStages]), (count / kVStages) & 1);
+        if (more) ok = ok && warp_wait(smem_u32(&ms.k_full[n % kKStages]), (n / kKStages) & 1);
+        ok = ok && warp_wait(smem_u32(&ms.p_ready[0]), count & 1);
         if (!ok) break;
         umma::fence_after();
-        qk(0, count);
-        if (two) qk(1, count);
-        umma::commit(smem_u32(&ms.k_empty[count % kKStages]));
-        for (int t = 0; t < w.nt && ok; ++t, ++count) {
-          const bool more = t + 1 < w.nt;
-          const int n = count + 1;
-          if (more) ok = mbar_wait(smem_u32(&ms.k_full[n % kKStages]), (n / kKStages) & 1);
-          if (ok) ok = mbar_wait(smem_u32(&ms.p_ready[0]), count & 1);
+        pv(0, count, t == 0, !more);                      // before the next S, which overwrites P
+        if (more) qk(0, n);
+        if (two) {
+          ok = warp_wait(smem_u32(&ms.p_ready[1]), count_b & 1);
           if (!ok) break;
+          ++count_b;
           umma::fence_after();
-          if (more) qk(0, n);
-          ok = mbar_wait(smem_u32(&ms.v_full), count & 1);
-          if (!ok) break;
-          umma::fence_after();
-          pv(0, t == 0);
-          if (two) {
-            ok = mbar_wait(smem_u32(&ms.p_ready[1]), count_b & 1);
-            if (!ok) break;
-            ++count_b;
-            umma::fence_after();
-            if (more) qk(1, n);
-          }
-          if (more) umma::commit(smem_u32(&ms.k_empty[n % kKStages]));
-          if (two) pv(1, t == 0);
-          umma::commit(smem_u32(&ms.v_empty));
+          pv(1, count, t == 0, !more);
+          if (more) qk(1, n);
         }
-        if (!ok) break;
-        ++seg;
-        if (two) ++seg_b;
-        w.next(a);
+        commit(on, smem_u32(&ms.v_empty[count % kVStages]));
+        if (more) commit(on, smem_u32(&ms.k_empty[n % kKStages]));
       }
-      if (!ok) paged_error(d, kErrTimeout);
-      umma::commit(smem_u32(&ms.drain));
-      mbar_wait(smem_u32(&ms.drain), 0);
+      if (!ok) break;
+      ++seg;
+      if (two) ++seg_b;
+      w.next(a);
     }
-    __syncwarp();
+    if (!ok && lane == 0) paged_error(d, kErrTimeout);
+    commit(on, smem_u32(&ms.drain));
+    mbar_wait(smem_u32(&ms.drain), 0);
   } else {
     // ---- softmax of tile x: a thread to a row
     const int x = warp >> 2, row = tid & 127;
@@ -456,8 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
     const int token = row / d.G, head = row % d.G;        // of the tile
     const float qk = kLog2e * rsqrtf((float)D);
     uint8_t* q_at = sq + x * C::Q + row * 16;
-    uint8_t* p_at = sp + x * C::P + row * 16;
-    int count = 0;
+    int count = 0, seg = 0;
     bool ok = true;
     float c = 0.f;
     // the row's query in two pieces, chunk by chunk of 16 dimensions
@@ -466,11 +539,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       const bool live = token < qpt && i < y.u.cnt;
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
           (live ? ((size_t)(y.q.first + y.u.i0 + i) * d.Hq + y.h * d.G + head) * D : 0));
+      uint4 raw[D / 8];                                   // all loads in flight at once
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) raw[j] = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
       float amax = 0.f;
-#pragma unroll 4
+#pragma unroll
       for (int j = 0; j < D / 8; ++j) {
-        const uint4 v = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&raw[j]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float2 f = __bfloat1622float2(p[u]);
@@ -480,13 +555,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       const int e = scale_exp(amax);
       const float up = exp2_int(-e);
       c = exp2_int(live ? e : 0) * qk;
-#pragma unroll 2
+#pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint4 v = live ? __ldg(src + 2 * j + k) : make_uint4(0, 0, 0, 0);
-          const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+          const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&raw[2 * j + k]);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const float2 f = __bfloat1622float2(p[2 * u]), g = __bfloat1622float2(p[2 * u + 1]);
@@ -520,92 +594,60 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       const int all_lo = a.window > 0 ? max(last - a.window, 0) : 0;
       for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
         const int slot = (tile + t - w.t0) % kScaleSlots;
-        ok = mbar_wait(smem_u32(&ms.s_ready[x]), count & 1);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(smem_u32(&ms.s_ready[x]), count & 1);
         if (!ok) break;
         umma::fence_after();
-        const int base = (w.u.b0 + t * kTileBlocks) * kBlock;
-        const int bad = ms.bad[slot];
-        const bool masked = base < all_lo || base + kTile > all_hi || bad;
-        // the row's maximum, from each block's largest product
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float s[32];
-          umma::ld32(t_s + 32 * j, s);
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const int pos = base + 32 * j + k;
-              if (pos >= hi || pos < lo || (bad >> (2 * j + k / 16) & 1)) s[k] = -INFINITY;
-            }
+        Tile y;
+        *reinterpret_cast<float4*>(y.ks) = *reinterpret_cast<const float4*>(ms.ks[slot]);
+        *reinterpret_cast<float4*>(y.ks + 4) = *reinterpret_cast<const float4*>(ms.ks[slot] + 4);
+        *reinterpret_cast<float4*>(y.vs) = *reinterpret_cast<const float4*>(ms.vs[slot]);
+        *reinterpret_cast<float4*>(y.vs + 4) = *reinterpret_cast<const float4*>(ms.vs[slot] + 4);
+        y.base = (w.u.b0 + t * kTileBlocks) * kBlock;
+        y.lo = lo;
+        y.hi = hi;
+        y.bad = ms.bad[slot];
+        const bool masked = y.base < all_lo || y.base + kTile > all_hi || y.bad;
+        uint32_t h[64];
+        float f = 1.f, add, big;
+        // a new maximum: the first one, or one that passes the last by the slack
+        auto move = [&](float top) {
+          if (top > m + kSlack || (m == -INFINITY && top > -INFINITY)) {
+            f *= m == -INFINITY ? 0.f : ex2(m - top);
+            m = top;
           }
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            float v = s[16 * b];
-#pragma unroll
-            for (int k = 1; k < 16; ++k) v = fmaxf(v, s[16 * b + k]);
-            const float tb = fmaf(v, ms.ks[slot][2 * j + b] * c, ms.ev[slot][2 * j + b]);
-            top = fmaxf(top, v == -INFINITY ? -INFINITY : tb);
+        };
+        auto ref = [&] { return (m == -INFINITY ? 0.f : m) - kTop; };
+        if (masked) {
+          move(row_max<true>(t_s, y, c));
+          add = row_exp<true>(t_s, y, c, ref(), h, big);
+        } else {
+          // Within a segment the last maximum mostly serves: the exponentials are taken at once, and
+          // again only if a block's sum passes what the slack allows (or overflows).
+          bool again = t == w.t0 || __any_sync(0xffffffffu, m == -INFINITY);
+          if (!again) {
+            add = row_exp<false>(t_s, y, c, ref(), h, big);
+            again = __any_sync(0xffffffffu, !(big <= kLimit));
           }
-        }
-        float f = 1.f;
-        if (top > m + kSlack || (m == -INFINITY && top > -INFINITY)) {
-          f = ex2(m - top);                               // 0 the first time
-          m = top;
-        }
-        const float ref = (m == -INFINITY ? 0.f : m) - kTop;
-        // the previous product is done with the probabilities' buffer and the output
-        if (t > w.t0) {
-          ok = mbar_wait(smem_u32(&ms.pv_done[x]), (count - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          umma::fence_after();
-          if (__any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-            for (int j = 0; j < D; j += 16) {
-              float o[16];
-              ld16(t_o + j, o);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= f;
-              st16(t_o + j, o);
-            }
-            wait_st();
+          if (again) {
+            move(row_max<false>(t_s, y, c));
+            add = row_exp<false>(t_s, y, c, ref(), h, big);
           }
         }
-        l *= f;
+        l = fmaf(l, f, add);
+        // S was issued behind the previous product, so that is done with P and O
+        if (t > w.t0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float s[32];
-          umma::ld32(t_s + 32 * j, s);
+          for (int j = 0; j < D; j += 16) {
+            float o[16];
+            ld16(t_o + j, o);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float mul = ms.ks[slot][2 * j + b] * c, sub = ms.ev[slot][2 * j + b] - ref;
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float v = ex2(fmaf(s[16 * b + k], mul, sub));
-              if (masked) {
-                const int pos = base + 32 * j + 16 * b + k;
-                if (pos >= hi || pos < lo || (bad >> (2 * j + b) & 1)) v = 0.f;
-              }
-              s[16 * b + k] = v;
-              sum += v;
-            }
-            l = fmaf(sum, ms.iv[slot][2 * j + b], l);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {                   // 8 tokens to a 16-byte operand row
-            uint32_t h[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const __half2 y = __floats2half2_rn(s[8 * k + 2 * u], s[8 * k + 2 * u + 1]);
-              h[u] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            *reinterpret_cast<uint4*>(p_at + (size_t)(4 * j + k) * (kRows * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int k = 0; k < 16; ++k) o[k] *= f;
+            st16(t_o + j, o);
           }
         }
-        umma::fence_async_smem();
+        st32(t_s, h);                                     // P over S, two tokens to a column
+        st32(t_s + 32, h + 32);
+        wait_st();
         umma::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready[x]));
@@ -617,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       w.next(a);
       while (w.left > 0 && !mine(w)) { tile += w.nt; w.next(a); }
       if (w.left > 0) load_q(w);
-      ok = mbar_wait(smem_u32(&ms.pv_done[x]), (count - 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = warp_wait(smem_u32(&ms.o_done[x]), seg & 1);
+      ++seg;
       if (!ok) break;
       umma::fence_after();
       if (y.whole) {
@@ -647,9 +689,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
           float o[16];
           ld16(t_o + j, o);
           if (live) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + rec * D + j);
+            float4* dst = reinterpret_cast<float4*>(a.part_o) + (rec - row) * (D / 4) + (j / 4) * kRows + row;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 4; ++k) dst[k * kRows] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
         if (live) a.part_ml[rec] = make_float2(m, l);
@@ -691,29 +733,45 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAt
   const int c0 = c - 1;
   int c1 = c;
   while (c1 + 1 < ctas && total * (c1 + 1) / ctas < off + u.tiles) ++c1;
-  for (int k = 0; k < kJoinRows; ++k) {
-    const int pr = blockIdx.y * kJoinRows + k, x = pr / kRows, row = pr % kRows;   // of the unit's 256 rows
-    const int i = x * qpt + row / d.G;
-    if (row / d.G >= qpt || i >= u.cnt) continue;
-    auto rec_of = [&](int e) {
-      const bool first = off <= total * e / ctas;         // the unit is the CTA's first
-      return ((size_t)(2 * e + (first ? 0 : 1)) * 2 + x) * kRows + row;
-    };
-    float top = -INFINITY;
-    for (int e = c0; e <= c1; ++e) top = fmaxf(top, a.part_ml[rec_of(e)].x);
-    const float ref = top > -INFINITY ? top : 0.f;
-    float sum = 0.f, acc = 0.f;
-#pragma unroll 4
-    for (int e = c0; e <= c1; ++e) {
-      const size_t rec = rec_of(e);
-      const float2 ml = a.part_ml[rec];
-      const float f = ex2(ml.x - ref);
-      sum = fmaf(ml.y, f, sum);
-      if (threadIdx.x < D) acc = fmaf(a.part_o[rec * D + threadIdx.x], f, acc);
+  // a thread has four dimensions of a row; partials are [tile][D / 4][128 rows][4]
+  const int pr = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, x = pr / kRows, row = pr % kRows;
+  const int i = x * qpt + row / d.G;
+  if (row / d.G >= qpt || i >= u.cnt) return;
+  auto rec_of = [&](int e) {
+    const bool first = off <= total * e / ctas;           // the unit is the CTA's first
+    return ((size_t)(2 * e + (first ? 0 : 1)) * 2 + x) * kRows;
+  };
+  float top = -INFINITY, sum = 0.f;
+  for (int e = c0; e <= c1; ++e) top = fmaxf(top, a.part_ml[rec_of(e) + row].x);
+  const float ref = top > -INFINITY ? top : 0.f;
+  float4 acc[D / 64];
+#pragma unroll
+  for (int q4 = 0; q4 < D / 64; ++q4) acc[q4] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int e = c0; e <= c1; ++e) {
+    const size_t rec = rec_of(e);
+    const float2 ml = a.part_ml[rec + row];
+    const float f = ex2(ml.x - ref);
+    sum = fmaf(ml.y, f, sum);
+#pragma unroll
+    for (int q4 = 0; q4 < D / 64; ++q4) {
+      const float4 v = reinterpret_cast<const float4*>(a.part_o)[rec * (D / 4) + (threadIdx.x / kJoinRows + 16 * q4) * kRows + row];
+      acc[q4].x = fmaf(v.x, f, acc[q4].x);
+      acc[q4].y = fmaf(v.y, f, acc[q4].y);
+      acc[q4].z = fmaf(v.z, f, acc[q4].z);
+      acc[q4].w = fmaf(v.w, f, acc[q4].w);
     }
-    if (threadIdx.x < D)
-      static_cast<__nv_bfloat16*>(a.out)[((size_t)(q.first + u.i0 + i) * d.Hq + search.h * d.G + row % d.G) * D + threadIdx.x] =
-          __float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                       ((size_t)(q.first + u.i0 + i) * d.Hq + search.h * d.G + row % d.G) * D;
+#pragma unroll
+  for (int q4 = 0; q4 < D / 64; ++q4) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[q4].x * inv, acc[q4].y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[q4].z * inv, acc[q4].w * inv);
+    uint2 raw;
+    raw.x = *reinterpret_cast<const uint32_t*>(&lo);
+    raw.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(out + (threadIdx.x / kJoinRows + 16 * q4) * 4) = raw;
   }
 }
 
