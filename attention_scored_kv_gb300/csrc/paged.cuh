@@ -44,6 +44,8 @@ struct PagedAttend {
   float* blk;              // [n_reqs][table_stride][Hq] log2 of the blocks' weight sums (mass only)
   float* lse;              // [n_reqs][Hq] log2 of the rows' sums (mass only)
   int32_t splits;          // general kernel: parts of a row's range
+  uint8_t* q_pieces;       // prompt kernel: split queries, and their rows' factors
+  float* q_factors;
 };
 
 // How a call runs: a pure function of host-known sizes, so that the scratch size and the
@@ -53,7 +55,7 @@ struct PagedAttendPlan {
   int splits;              // general kernel
   int rows;                // decode kernel: query rows of a unit
   int grid;                // decode and prompt kernels
-  size_t part_o, part_ml, blk, lse, total;   // scratch offsets
+  size_t part_o, part_ml, blk, lse, q_pieces, q_factors, total;   // scratch offsets
 };
 
 __host__ __device__ inline size_t k_code(int D, int t, int d) {
@@ -79,6 +81,17 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes16) {
   const uint16_t c = (uint16_t)codes16;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t codes16) {
+  uint32_t h;
+  const uint16_t c = (uint16_t)codes16;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return *reinterpret_cast<const __half2*>(&h);
+}
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(__half2 v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&v)));
+  return r;
 }
 // Codes of (lo, hi), round to nearest even, saturating.
 __device__ __forceinline__ uint32_t float2_to_e4m3x2(float lo, float hi) {
@@ -122,6 +135,8 @@ cudaError_t launch_paged_gather(const PagedDev& d, int layer, int n_rows, const 
 int paged_decode_ctas_per_sm();
 cudaError_t launch_paged_decode(const PagedAttend& a, int rows, int grid, cudaStream_t st);
 int paged_prompt_rows();
+int paged_prompt_tiles(int G, int n_reqs, int total_q);
+size_t paged_prompt_tile_bytes(int D);
 cudaError_t launch_paged_prompt(const PagedAttend& a, int grid, cudaStream_t st);
 cudaError_t launch_paged_general(const PagedAttend& a, cudaStream_t st);
 cudaError_t launch_paged_mass(const PagedAttend& a, cudaStream_t st);

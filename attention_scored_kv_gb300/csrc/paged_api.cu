@@ -143,7 +143,10 @@ PagedAttendPlan plan_attend(const kvs_paged* pc, int n_reqs, int stride, int tot
   p.part_ml = p.part_o + up(recs * d.D * sizeof(float));
   p.blk = p.part_ml + up(recs * sizeof(float2));
   p.lse = p.blk + (mass ? up((size_t)n_reqs * stride * d.Hq * sizeof(float)) : 0);
-  p.total = p.lse + (mass ? up((size_t)n_reqs * d.Hq * sizeof(float)) : 0);
+  p.q_pieces = p.lse + (mass ? up((size_t)n_reqs * d.Hq * sizeof(float)) : 0);
+  const size_t tiles = p.kernel == PagedAttendPlan::kPrompt ? (size_t)paged_prompt_tiles(d.G, n_reqs, total_q) * d.Hkv : 0;
+  p.q_factors = p.q_pieces + up(tiles * paged_prompt_tile_bytes(d.D));
+  p.total = p.q_factors + up(tiles * (paged_prompt_rows() / 2) * sizeof(float));
   return p;
 }
 
@@ -363,6 +366,8 @@ kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const 
   a.blk = d_block_mass_opt ? reinterpret_cast<float*>(s + p.blk) : nullptr;
   a.lse = d_block_mass_opt ? reinterpret_cast<float*>(s + p.lse) : nullptr;
   a.splits = p.splits;
+  a.q_pieces = s + p.q_pieces;
+  a.q_factors = reinterpret_cast<float*>(s + p.q_factors);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = p.kernel == PagedAttendPlan::kDecode   ? launch_paged_decode(a, p.rows, p.grid, cs)
                   : p.kernel == PagedAttendPlan::kPrompt ? launch_paged_prompt(a, p.grid, cs)

@@ -32,15 +32,19 @@ namespace {
 using namespace pmma;
 
 constexpr int kTile = 128, kTileBlocks = kTile / kBlock;
-constexpr int kThreads = 384;            // 8 softmax warps, K copies, matrix, 2 V warps
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kVWarp = 10, kVThreads = 64;
-constexpr int kKStages = 3, kVStages = 2, kScaleSlots = 4;
+constexpr int kThreads = 512;            // 8 softmax warps, K copies, matrix, query copies, a spare, 4 V warps
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10, kVWarp = 12, kVThreads = 128;
+// Registers of a softmax thread and of the others: 256 (168 + 88) = the block's 65536.
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
+constexpr int kKStages = 3, kVStages = 1, kQStages = 2;
+constexpr int kSlots = 4;                // scales of this many tiles, row factors of this many segments
+constexpr int kSetup = 2;                // what a unit's start costs, in tiles, where work is cut
 constexpr int kRows = 128;               // rows of a tile of queries
 constexpr int kChunk = 512;              // requests of one round of the search
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTop = 6.f;              // x of the maximum when it was taken: 2^6
-constexpr float kSlack = 8.f;            // the maximum moves when a row passes it by this
-constexpr float kLimit = 16384.f;        // 2^(kTop + kSlack): more in a block's sum, and the maximum is looked at
+constexpr float kTop = 0.f;              // x of the maximum when it was taken: 1
+constexpr float kSlack = 15.f;           // the maximum moves when a row passes it by this: x <= 2^15 fits f16
+constexpr float kLimit = 32768.f;        // 2^(kTop + kSlack): more in a block's sum, and the maximum is looked at
 
 // Units of request r: groups of `per` query tokens, all KV heads alike.
 struct Req {
@@ -62,6 +66,7 @@ __device__ __forceinline__ Req req_of(const PagedAttend& a, int r) {
 struct Unit {
   int i0, cnt;           // first query token of the request, tokens
   int b0, nb, tiles;     // blocks that any of them sees
+  __device__ int cost() const { return tiles + kSetup; }
 };
 __device__ __forceinline__ Unit unit_of(const PagedAttend& a, const Req& x, int qg, int per) {
   Unit u;
@@ -82,17 +87,17 @@ struct Search {
   int r, qg, h, t;
 };
 
-// Tiles of request r per KV head, by a warp.
+// Cost of request r per KV head, by a warp: tiles and units' starts.
 __device__ int request_tiles(const PagedAttend& a, int r, int per) {
   const Req x = req_of(a, r);
   int sum = 0;
-  for (int qg = threadIdx.x & 31; qg * per < x.n; qg += 32) sum += unit_of(a, x, qg, per).tiles;
+  for (int qg = threadIdx.x & 31; qg * per < x.n; qg += 32) sum += unit_of(a, x, qg, per).cost();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
 }
 
-// Total tiles of the call, by a block of `warps` warps.
+// Total cost of the call, by a block of `warps` warps.
 __device__ long long total_tiles(const PagedAttend& a, int per, int warps, Search& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long sum = 0;
@@ -108,8 +113,8 @@ __device__ long long total_tiles(const PagedAttend& a, int per, int warps, Searc
   return sum * a.d.Hkv;
 }
 
-// Where tile `target` of the call is: s.r, s.qg, s.h, s.t (tile within the unit), for all
-// threads.  After total_tiles, which left the first kChunk requests' counts.
+// Where `target` of the call's cost is: s.r, s.qg, s.h, s.t (within the unit: its start, then
+// its tiles), for all threads.  After total_tiles, which left the first kChunk requests' counts.
 __device__ void locate(const PagedAttend& a, int per, int warps, long long target, Search& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hkv = a.d.Hkv;
   long long base = 0;
@@ -152,7 +157,7 @@ __device__ void locate(const PagedAttend& a, int per, int warps, long long targe
     long long at = s.before;
     for (int q0 = 0; q0 * per < x.n; q0 += 32) {
       const int qg = q0 + lane;
-      const int tiles = qg * per < x.n ? unit_of(a, x, qg, per).tiles : 0;
+      const int tiles = qg * per < x.n ? unit_of(a, x, qg, per).cost() : 0;
       const long long mine = (long long)tiles * hkv;
       long long upto = mine;
 #pragma unroll
@@ -173,29 +178,38 @@ __device__ void locate(const PagedAttend& a, int per, int warps, long long targe
   __syncthreads();
 }
 
-// A CTA's walk over its tiles, segment by segment (a segment: tiles of one unit).
+// A CTA's walk over its share of the cost, segment by segment (a segment: tiles of one unit).
+// A share that ends within a unit's start leaves the unit to the next CTA.
 struct Walk {
-  int r, qg, h, t0, nt, left, per;
+  int r, qg, h, v0, left, per, seg;        // v0: where the share enters the unit's cost; left: from there on
+  int t0, nt;                              // the segment's tiles of the unit: [t0, t0 + nt); 0: no more
+  int done;                                // tiles of the CTA before it
   Req q;
   Unit u;
   bool first, whole;
-  __device__ void start(const PagedAttend& a, const Search& s, int tiles, int per_) {
-    r = s.r; qg = s.qg; h = s.h; t0 = s.t;
-    left = tiles;
+  __device__ void start(const PagedAttend& a, const Search& s, int cost, int per_) {
+    r = s.r; qg = s.qg; h = s.h; v0 = s.t;
+    left = cost;
     per = per_;
     first = true;
+    seg = done = 0;
     q = req_of(a, r);
     u = unit_of(a, q, qg, per);
     clip();
   }
   __device__ void clip() {
-    nt = min(u.tiles - t0, left);
+    const int v1 = min(u.cost(), v0 + left);
+    t0 = max(v0 - kSetup, 0);
+    nt = max(v1 - kSetup - t0, 0);
     whole = nt == u.tiles;
   }
   __device__ void next(const PagedAttend& a) {
-    left -= nt;
+    left -= u.cost() - v0;
+    done += nt;
     first = false;
-    t0 = 0;
+    nt = 0;
+    v0 = 0;
+    ++seg;
     if (left <= 0) return;
     if (++h == a.d.Hkv) {
       h = 0;
@@ -212,10 +226,14 @@ struct Walk {
 
 struct Misc {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], drain;
-  uint64_t s_ready[2], p_ready[2], o_done[2], q_ready[2];
+  uint64_t s_ready[2], p_ready[2], o_done[2];
+  uint64_t q_ready[kSlots], q_empty[kQStages], sc_ready[kSlots];
   uint32_t tmem;
-  alignas(16) float ks[kScaleSlots][kTileBlocks], vs[kScaleSlots][kTileBlocks];
-  int bad[kScaleSlots];                    // blocks of the tile that are not a page, as bits
+  alignas(16) float ks[kSlots][kTileBlocks], vs[kSlots][kTileBlocks];
+  int bad[kSlots];                         // blocks of the tile that are not a page, as bits
+  alignas(16) float qc[kSlots][2 * kRows]; // of each row: its query's scale, log2(e) / sqrt(D)
+  Walk walk[8][2];                         // the softmax warps' segments, this one and the next (they would cost
+                                           // the tile loop 20 registers)
 };
 
 template <int D>
@@ -224,7 +242,7 @@ struct Cfg {
   static constexpr int Q = kRows * 2 * D;                 // one tile of queries, both pieces
   static constexpr int K = kTileBlocks * PAGE;            // a stage of K
   static constexpr int V = kTile * D * 2;                 // V as f16
-  static constexpr int BODY = 2 * Q + kKStages * K + kVStages * V;
+  static constexpr int BODY = kQStages * 2 * Q + kKStages * K + kVStages * V;
   static constexpr int SMEM = BODY + (int)sizeof(Misc) + 1024;
   static_assert(SMEM + (int)sizeof(Search) <= 227 * 1024, "shared memory");
 };
@@ -232,10 +250,18 @@ struct Cfg {
 // What a row's thread needs of a tile of 128 tokens: the blocks' scales and what it sees.
 struct Tile {
   float ks[kTileBlocks], vs[kTileBlocks];  // in registers: the operands' traffic starves shared-memory loads
-  int base, lo, hi;      // first position; the row sees [lo, hi)
-  uint32_t bad;          // blocks that are not a page
-  __device__ __forceinline__ bool hidden(int k) const {
-    return base + k >= hi || base + k < lo || (bad >> (k >> 4) & 1);
+  uint32_t seen[4];      // where the tile is masked: the tokens that the row sees, as bits
+  __device__ __forceinline__ bool hidden(int k) const { return !(seen[k >> 5] >> (k & 31) & 1); }
+  __device__ __forceinline__ void look(int base, int lo, int hi, uint32_t bad) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int up = hi - base - 32 * j, down = lo - base - 32 * j;      // sees bits [down, up)
+      uint32_t v = up >= 32 ? ~0u : up <= 0 ? 0u : (1u << up) - 1;
+      v &= down <= 0 ? ~0u : down >= 32 ? 0u : ~0u << down;
+      if (bad >> (2 * j) & 1) v &= 0xffff0000u;
+      if (bad >> (2 * j + 1) & 1) v &= 0xffffu;
+      seen[j] = v;
+    }
   }
   __device__ __forceinline__ float ev(int b) const { return (float)((__float_as_int(vs[b]) >> 23) - 127); }
   __device__ __forceinline__ float iv(int b) const { return __int_as_float((254 << 23) - __float_as_int(vs[b])); }
@@ -305,6 +331,63 @@ __device__ __forceinline__ float row_exp(uint32_t t_s, const Tile& y, float c, f
   return l;
 }
 
+// Place of a tile of queries among the split ones, from its first packed row: a request's tiles are
+// neighbours, and no two requests' meet.
+__device__ __forceinline__ int query_tile(int row, int r, int qpt) { return row / qpt + r; }
+
+// Splits the queries once: for each (tile, KV head) [16-byte chunk][128 rows][16 bytes], the first pieces' D / 16
+// chunks and then the second's, and each row's factor.  Grid: tiles, KV heads; a thread to a row.
+template <int D>
+__global__ void __launch_bounds__(kRows) split_kernel(const PagedAttend a, const int qpt) {
+  launch_dependents();
+  const PagedDev& d = a.d;
+  const int row = threadIdx.x, h = blockIdx.y, id = blockIdx.x;
+  // the last request whose first tile is at or before this one
+  int lo = 0, hi = a.n_reqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    const int first = a.row_start ? __ldg(a.row_start + mid) : mid;
+    if (query_tile(first, mid, qpt) <= id) lo = mid; else hi = mid - 1;
+  }
+  const Req q = req_of(a, lo);
+  const int i0 = (id - query_tile(q.first, lo, qpt)) * qpt;
+  if (i0 < 0 || i0 >= q.n) return;
+  const int i = i0 + row / d.G;
+  const bool live = row / d.G < qpt && i < q.n;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+      (live ? ((size_t)(q.first + i) * d.Hq + h * d.G + row % d.G) * D : 0));
+  uint4 raw[D / 8];
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) raw[j] = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+  __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) top2 = __hmax2(top2, __habs2(reinterpret_cast<const __nv_bfloat162*>(&raw[j])[u]));
+  const int e = scale_exp(fmaxf(__low2float(top2), __high2float(top2)));
+  const uint64_t up = pack2(exp2_int(-e), exp2_int(-e));
+  const size_t at = (size_t)id * d.Hkv + h;
+  a.q_factors[at * kRows + row] = exp2_int(live ? e : 0) * (kLog2e * rsqrtf((float)D));
+  uint8_t* out = a.q_pieces + at * (kRows * 2 * D) + row * 16;
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    uint32_t hi4[4], lo4[4];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      // scaled, an element is at most 448 and has 8 bits: f16 holds it and its first piece's remainder exactly
+      const uint32_t two = reinterpret_cast<const uint32_t*>(&raw[2 * j + u / 4])[u % 4];
+      const float2 f = unpack2(mul2(pack2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u)), up));
+      const __half2 v = __floats2half2_rn(f.x, f.y);
+      const uint32_t c1 = f16x2_to_e4m3x2(v);
+      const uint32_t c2 = f16x2_to_e4m3x2(__hsub2(v, e4m3x2_to_half2(c1)));
+      hi4[u / 2] = u & 1 ? hi4[u / 2] | c1 << 16 : c1;
+      lo4[u / 2] = u & 1 ? lo4[u / 2] | c2 << 16 : c2;
+    }
+    *reinterpret_cast<uint4*>(out + (size_t)j * (kRows * 16)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+    *reinterpret_cast<uint4*>(out + (size_t)(j + D / 16) * (kRows * 16)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a, const int qpt) {
   using C = Cfg<D>;
@@ -312,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
   __shared__ Search search;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sq = smem;
-  uint8_t* sk = sq + 2 * C::Q;
+  uint8_t* sk = sq + kQStages * 2 * C::Q;
   uint8_t* sv = sk + kKStages * C::K;
   Misc& ms = *reinterpret_cast<Misc*>(sv + kVStages * C::V);
   const PagedDev& d = a.d;
@@ -341,7 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       mbar_init(smem_u32(&ms.s_ready[i]), 1);
       mbar_init(smem_u32(&ms.p_ready[i]), 4);
       mbar_init(smem_u32(&ms.o_done[i]), 1);
-      mbar_init(smem_u32(&ms.q_ready[i]), 4);
+      mbar_init(smem_u32(&ms.q_empty[i]), 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&ms.q_ready[i]), 1);
+      mbar_init(smem_u32(&ms.sc_ready[i]), 1);
     }
     mbar_fence_init();
   }
@@ -357,12 +444,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
   w.start(a, search, (int)(end - begin), per);
 
   if (warp == kCopyWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
     // ---- K pages and the blocks' scales: lane j < 8 has block j of the tile
     const uint8_t* kbase = d.k + a.layer * d.layer_bytes;
     const float2* sbase = d.scales + a.layer * d.layer_scales;
     int count = 0;
     bool ok = true;
-    while (w.left > 0 && ok) {
+    while (w.nt > 0 && ok) {
       const int32_t* row = a.table + (size_t)w.r * a.table_stride;
       auto fetch = [&](int t, int& nb, int& page, float2& sc) {
         const int b = w.u.b0 + t * kTileBlocks;
@@ -385,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       float2 sc;
       fetch(w.t0, nb, page, sc);
       for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
-        const int st = count % kKStages, slot = count % kScaleSlots;
+        const int st = count % kKStages, slot = count % kSlots;
         if (count >= kKStages) ok = mbar_wait(smem_u32(&ms.k_empty[st]), (count / kKStages - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -400,40 +488,69 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
         }
         if (lane == 0) ms.bad[slot] = (int)(~good & 0xffu);
         __syncwarp();
-        if (lane == 0) mbar_arrive(full);
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ms.sc_ready[slot]));
+          mbar_arrive(full);
+        }
         if (t + 1 < w.t0 + w.nt) fetch(t + 1, nb, page, sc);
       }
       if (ok) w.next(a);
     }
     if (!ok && lane == 0) paged_error(d, kErrTimeout);
     for (int i = max(0, count - kKStages); i < count; ++i) mbar_wait(smem_u32(&ms.k_full[i % kKStages]), (i / kKStages) & 1);
+  } else if (warp == kQWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
+    // ---- the next segment's queries and row factors, as the split kernel left them
+    bool ok = true;
+    wait_previous();
+    while (w.nt > 0 && ok) {
+      const int buf = w.seg % kQStages, slot = w.seg % kSlots, tiles = w.u.cnt > qpt ? 2 : 1;
+      if (w.seg >= kQStages) ok = warp_wait(smem_u32(&ms.q_empty[buf]), (w.seg / kQStages - 1) & 1);
+      if (!ok) break;
+      const uint32_t full = smem_u32(&ms.q_ready[slot]);
+      if (lane == 0) mbar_expect(full, tiles * (C::Q + kRows * 4));
+      __syncwarp();
+      if (lane < tiles) {
+        const size_t at = (size_t)(query_tile(w.q.first + w.u.i0 + lane * qpt, w.r, qpt)) * d.Hkv + w.h;
+        bulk_load(smem_u32(sq + (buf * 2 + lane) * C::Q), a.q_pieces + at * C::Q, C::Q, full);
+        bulk_load(smem_u32(&ms.qc[slot][lane * kRows]), a.q_factors + at * kRows, kRows * 4, full);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
+      w.next(a);
+    }
+    if (!ok && lane == 0) paged_error(d, kErrTimeout);
+    // copies still in flight land before the CTA ends
+    for (int i = max(0, w.seg - kQStages); i < w.seg; ++i) mbar_wait(smem_u32(&ms.q_ready[i % kSlots]), (i / kSlots) & 1);
+  } else if (warp == kQWarp + 1) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
   } else if (warp >= kVWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
     // ---- V: a page's row d (16 tokens of a dimension) becomes two 16-byte operand rows
-    constexpr int DPT = D / kVThreads;                    // dimensions of a thread
-    constexpr int NI = kTileBlocks * DPT;
-    const int vt = tid - kVWarp * 32;
+    constexpr int PPI = kVThreads / D;                    // pages of one pass of the threads
+    constexpr int NI = kTileBlocks / PPI;
+    const int vt = tid - kVWarp * 32, dim = vt % D, pp = vt / D;
     const uint8_t* vbase = d.v + a.layer * d.layer_bytes;
     int count = 0;
     bool ok = true;
     uint4 raw[NI];
-    auto fetch = [&](const Walk& x, int t) {
-      const int b = x.u.b0 + t * kTileBlocks;
-      const int32_t* row = a.table + (size_t)x.r * a.table_stride;
-      int page[kTileBlocks];
-#pragma unroll
-      for (int j = 0; j < kTileBlocks; ++j) page[j] = b + j < x.u.b0 + x.u.nb ? __ldg(row + b + j) : -1;
+    auto fetch = [&](int t) {
+      const int b = w.u.b0 + t * kTileBlocks;
+      const int32_t* row = a.table + (size_t)w.r * a.table_stride;
+      int page[NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int pg = page[i / DPT], dim = vt + (i % DPT) * kVThreads;
-        raw[i] = pg >= 0 && pg < d.num_pages
-                     ? __ldg(reinterpret_cast<const uint4*>(vbase + ((size_t)pg * d.Hkv + x.h) * C::PAGE + dim * 16))
-                     : make_uint4(0, 0, 0, 0);
+        const int j = i * PPI + pp;
+        page[i] = b + j < w.u.b0 + w.u.nb ? __ldg(row + b + j) : -1;
       }
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        raw[i] = page[i] >= 0 && page[i] < d.num_pages
+                     ? __ldg(reinterpret_cast<const uint4*>(vbase + ((size_t)page[i] * d.Hkv + w.h) * C::PAGE + dim * 16))
+                     : make_uint4(0, 0, 0, 0);
     };
-    fetch(w, w.t0);
-    while (w.left > 0 && ok) {
-      Walk x = w;
-      x.next(a);
+    fetch(w.t0);
+    while (w.nt > 0 && ok) {
       for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
         const int st = count % kVStages;
         if (count >= kVStages) ok = warp_wait(smem_u32(&ms.v_empty[st]), (count / kVStages - 1) & 1);
@@ -447,27 +564,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * u]) : "h"((uint16_t)(c[u] & 0xffffu)));
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * u + 1]) : "h"((uint16_t)(c[u] >> 16)));
           }
-          uint4* dst = reinterpret_cast<uint4*>(sv + st * C::V + (size_t)(2 * (i / DPT)) * (D * 16) + (vt + (i % DPT) * kVThreads) * 16);
+          uint4* dst = reinterpret_cast<uint4*>(sv + st * C::V + (size_t)(2 * (i * PPI + pp)) * (D * 16) + dim * 16);
           dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
           dst[D] = make_uint4(h[4], h[5], h[6], h[7]);    // the next 8 tokens
         }
         umma::fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ms.v_full[st]));
-        if (t + 1 < w.t0 + w.nt) fetch(w, t + 1);
-        else if (x.left > 0) fetch(x, x.t0);
+        if (t + 1 < w.t0 + w.nt) fetch(t + 1);
       }
-      w = x;
+      if (ok) {
+        w.next(a);
+        if (w.nt > 0) fetch(w.t0);
+      }
     }
     if (!ok && lane == 0) paged_error(d, kErrTimeout);
   } else if (warp == kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
     // ---- matrix instructions
     constexpr uint32_t id_qk = idesc_e4m3(128, 128), id_pv = umma::idesc_f16(false, 128, D);
     const uint32_t on = elect();
-    int count = 0, seg = 0, count_b = 0, seg_b = 0;
+    int count = 0, count_b = 0;
     bool ok = true;
     auto qk = [&](int x, int n) {                         // S of tile x from K number n
-      const uint32_t aq = desc_lo(smem_u32(sq + x * C::Q), kRows * 16);
+      const uint32_t aq = desc_lo(smem_u32(sq + (w.seg % kQStages * 2 + x) * C::Q), kRows * 16);
       const uint32_t bk = desc_lo(smem_u32(sk + (n % kKStages) * C::K), 128);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)                    // the pieces hi, then lo, over the same K
@@ -483,16 +603,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
                    !(fresh && k == 0));
       if (last) commit(on, smem_u32(&ms.o_done[x]));
     };
-    while (w.left > 0 && ok) {
+    while (w.nt > 0 && ok) {
       const bool two = w.u.cnt > qpt;
-      ok = warp_wait(smem_u32(&ms.q_ready[0]), seg & 1);
-      if (two) ok = ok && warp_wait(smem_u32(&ms.q_ready[1]), seg_b & 1);
+      ok = warp_wait(smem_u32(&ms.q_ready[w.seg % kSlots]), (w.seg / kSlots) & 1);
       ok = ok && warp_wait(smem_u32(&ms.k_full[count % kKStages]), (count / kKStages) & 1);
       if (!ok) break;
       umma::fence_after();
       qk(0, count);
       if (two) qk(1, count);
       commit(on, smem_u32(&ms.k_empty[count % kKStages]));
+      if (w.nt == 1) commit(on, smem_u32(&ms.q_empty[w.seg % kQStages]));
       for (int t = 0; t < w.nt && ok; ++t, ++count) {
         const bool more = t + 1 < w.nt;
         const int n = count + 1;
@@ -513,129 +633,87 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
         }
         commit(on, smem_u32(&ms.v_empty[count % kVStages]));
         if (more) commit(on, smem_u32(&ms.k_empty[n % kKStages]));
+        if (t + 2 == w.nt) commit(on, smem_u32(&ms.q_empty[w.seg % kQStages]));
       }
       if (!ok) break;
-      ++seg;
-      if (two) ++seg_b;
       w.next(a);
     }
     if (!ok && lane == 0) paged_error(d, kErrTimeout);
     commit(on, smem_u32(&ms.drain));
     mbar_wait(smem_u32(&ms.drain), 0);
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
     // ---- softmax of tile x: a thread to a row
     const int x = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + x * 128 + lanes, t_o = tmem + 256 + x * 128 + lanes;
     const int token = row / d.G, head = row % d.G;        // of the tile
-    const float qk = kLog2e * rsqrtf((float)D);
-    uint8_t* q_at = sq + x * C::Q + row * 16;
-    int count = 0, seg = 0;
+    int count = 0, seg = 0;                               // tiles and segments that have this tile of queries
     bool ok = true;
-    float c = 0.f;
-    // the row's query in two pieces, chunk by chunk of 16 dimensions
-    auto load_q = [&](const Walk& y) {
-      const int i = x * qpt + token;
-      const bool live = token < qpt && i < y.u.cnt;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-          (live ? ((size_t)(y.q.first + y.u.i0 + i) * d.Hq + y.h * d.G + head) * D : 0));
-      uint4 raw[D / 8];                                   // all loads in flight at once
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) raw[j] = live ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-      float amax = 0.f;
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&raw[j]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float2 f = __bfloat1622float2(p[u]);
-          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
+    // the next segment that has this tile (B may have none)
+    Walk* const walks = ms.walk[warp];
+    auto advance = [&](Walk& to, const Walk& from, bool step) {
+      if (lane == 0) {
+        to = from;
+        if (step) to.next(a);
+        while (to.nt > 0 && x == 1 && to.u.cnt <= qpt) to.next(a);
       }
-      const int e = scale_exp(amax);
-      const float up = exp2_int(-e);
-      c = exp2_int(live ? e : 0) * qk;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&raw[2 * j + k]);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float2 f = __bfloat1622float2(p[2 * u]), g = __bfloat1622float2(p[2 * u + 1]);
-            const uint32_t h0 = float2_to_e4m3x2(f.x * up, f.y * up), h1 = float2_to_e4m3x2(g.x * up, g.y * up);
-            const float2 b0 = e4m3x2_to_float2(h0), b1 = e4m3x2_to_float2(h1);
-            hi[2 * k + u] = h0 | h1 << 16;
-            lo[2 * k + u] = float2_to_e4m3x2(f.x * up - b0.x, f.y * up - b0.y) |
-                            float2_to_e4m3x2(g.x * up - b1.x, g.y * up - b1.y) << 16;
-          }
-        }
-        *reinterpret_cast<uint4*>(q_at + (size_t)j * (kRows * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(q_at + (size_t)(j + D / 16) * (kRows * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      umma::fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready[x]));
     };
-    auto mine = [&](const Walk& y) { return x == 0 || y.u.cnt > qpt; };
-    // the first segment that has this tile, and its place in the scale slots
-    int tile = 0;                                         // tiles of the CTA before the segment
-    while (w.left > 0 && !mine(w)) { tile += w.nt; w.next(a); }
-    if (w.left > 0) load_q(w);
-    while (w.left > 0 && ok) {
+    advance(walks[0], w, false);
+    for (; walks[seg & 1].nt > 0 && ok;) {
+      const Walk& w = walks[seg & 1];
+      float c = 0.f;
       float m = -INFINITY, l = 0.f;
       const int i = x * qpt + token;                      // the row's token of the unit
-      const bool live = token < qpt && i < w.u.cnt;
       const int hi = w.q.p0 + w.u.i0 + i + 1, lo = a.window > 0 ? hi - a.window : 0;
       // positions that all live rows of the tile see
       const int all_hi = w.q.p0 + w.u.i0 + x * qpt + 1;
       const int last = w.q.p0 + w.u.i0 + min(w.u.cnt, (x + 1) * qpt);
       const int all_lo = a.window > 0 ? max(last - a.window, 0) : 0;
-      for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
-        const int slot = (tile + t - w.t0) % kScaleSlots;
-        ok = warp_wait(smem_u32(&ms.s_ready[x]), count & 1);
-        if (!ok) break;
-        umma::fence_after();
+      int base = (w.u.b0 + w.t0 * kTileBlocks) * kBlock;
+      const int nt = w.nt, tile = w.done;
+      for (int t = 0; t < nt && ok; ++t, ++count, base += kTile) {
+        const int slot = (tile + t) % kSlots;
+        // The scales come ahead of S.  Not at a segment's start: B may skip segments, and is only sure of the
+        // barrier's phase once S is there; that is also where the row's factor is read.
+        if (t == 0) {
+          ok = warp_wait(smem_u32(&ms.s_ready[x]), count & 1);
+          c = ms.qc[w.seg % kSlots][x * kRows + row];
+        }
+        ok = ok && warp_wait(smem_u32(&ms.sc_ready[slot]), ((tile + t) / kSlots) & 1);
         Tile y;
         *reinterpret_cast<float4*>(y.ks) = *reinterpret_cast<const float4*>(ms.ks[slot]);
         *reinterpret_cast<float4*>(y.ks + 4) = *reinterpret_cast<const float4*>(ms.ks[slot] + 4);
         *reinterpret_cast<float4*>(y.vs) = *reinterpret_cast<const float4*>(ms.vs[slot]);
         *reinterpret_cast<float4*>(y.vs + 4) = *reinterpret_cast<const float4*>(ms.vs[slot] + 4);
-        y.base = (w.u.b0 + t * kTileBlocks) * kBlock;
-        y.lo = lo;
-        y.hi = hi;
-        y.bad = ms.bad[slot];
-        const bool masked = y.base < all_lo || y.base + kTile > all_hi || y.bad;
+        const uint32_t bad = ms.bad[slot];
+        const bool masked = base < all_lo || base + kTile > all_hi || bad;
+        if (masked) y.look(base, lo, hi, bad);
+        if (t > 0) ok = ok && warp_wait(smem_u32(&ms.s_ready[x]), count & 1);
+        if (!ok) break;
+        umma::fence_after();
         uint32_t h[64];
         float f = 1.f, add, big;
-        // a new maximum: the first one, or one that passes the last by the slack
-        auto move = [&](float top) {
-          if (top > m + kSlack || (m == -INFINITY && top > -INFINITY)) {
-            f *= m == -INFINITY ? 0.f : ex2(m - top);
-            m = top;
+        // Within a segment the last maximum mostly serves: the exponentials are taken at once, and
+        // again only if a block's sum passes what the slack allows (or overflows).
+        bool look = t == 0 || __any_sync(0xffffffffu, m == -INFINITY);
+        for (;;) {
+          if (look) {
+            const float top = masked ? row_max<true>(t_s, y, c) : row_max<false>(t_s, y, c);
+            if (top > m + kSlack || (m == -INFINITY && top > -INFINITY)) {
+              f = m == -INFINITY ? 0.f : ex2(m - top);
+              m = top;
+            }
           }
-        };
-        auto ref = [&] { return (m == -INFINITY ? 0.f : m) - kTop; };
-        if (masked) {
-          move(row_max<true>(t_s, y, c));
-          add = row_exp<true>(t_s, y, c, ref(), h, big);
-        } else {
-          // Within a segment the last maximum mostly serves: the exponentials are taken at once, and
-          // again only if a block's sum passes what the slack allows (or overflows).
-          bool again = t == w.t0 || __any_sync(0xffffffffu, m == -INFINITY);
-          if (!again) {
-            add = row_exp<false>(t_s, y, c, ref(), h, big);
-            again = __any_sync(0xffffffffu, !(big <= kLimit));
-          }
-          if (again) {
-            move(row_max<false>(t_s, y, c));
-            add = row_exp<false>(t_s, y, c, ref(), h, big);
-          }
+          const float ref = (m == -INFINITY ? 0.f : m) - kTop;
+          add = masked ? row_exp<true>(t_s, y, c, ref, h, big) : row_exp<false>(t_s, y, c, ref, h, big);
+          if (look || !__any_sync(0xffffffffu, !(big <= kLimit))) break;
+          look = true;
         }
         l = fmaf(l, f, add);
         // S was issued behind the previous product, so that is done with P and O
-        if (t > w.t0 && __any_sync(0xffffffffu, f != 1.f)) {
+        if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
           for (int j = 0; j < D; j += 16) {
             float o[16];
@@ -653,20 +731,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
         if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready[x]));
       }
       if (!ok) break;
-      // the next segment's queries while the last product runs
-      const Walk y = w;
-      tile += w.nt;
-      w.next(a);
-      while (w.left > 0 && !mine(w)) { tile += w.nt; w.next(a); }
-      if (w.left > 0) load_q(w);
+      advance(walks[(seg + 1) & 1], w, true);
       ok = warp_wait(smem_u32(&ms.o_done[x]), seg & 1);
-      ++seg;
       if (!ok) break;
       umma::fence_after();
-      if (y.whole) {
+      const bool live = token < qpt && i < w.u.cnt;
+      if (w.whole) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-            (live ? ((size_t)(y.q.first + y.u.i0 + i) * d.Hq + y.h * d.G + head) * D : 0);
+            (live ? ((size_t)(w.q.first + w.u.i0 + i) * d.Hq + w.h * d.G + head) * D : 0);
 #pragma unroll
         for (int j = 0; j < D; j += 16) {
           float o[16];
@@ -683,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
           }
         }
       } else {
-        const size_t rec = ((size_t)(2 * blockIdx.x + (y.first ? 0 : 1)) * 2 + x) * kRows + row;
+        const size_t rec = ((size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * 2 + x) * kRows + row;
 #pragma unroll
         for (int j = 0; j < D; j += 16) {
           float o[16];
@@ -697,6 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
         if (live) a.part_ml[rec] = make_float2(m, l);
       }
       umma::fence_before();
+      ++seg;
     }
     if (!ok && lane == 0) paged_error(d, kErrTimeout);
   }
@@ -723,8 +797,8 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAt
   if (work) {
     const long long begin = total * c / ctas;
     locate(a, per, kJoinThreads / 32, begin, search);
-    off = begin - search.t;                               // the unit's first tile
-    work = search.t > 0 && total * (c - 1) / ctas <= off;
+    off = begin - search.t;                               // the unit's start
+    work = search.t > kSetup && total * (c - 1) / ctas <= off + kSetup;
   }
   wait_previous();
   if (!work) return;
@@ -732,7 +806,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAt
   const Unit u = unit_of(a, q, search.qg, per);
   const int c0 = c - 1;
   int c1 = c;
-  while (c1 + 1 < ctas && total * (c1 + 1) / ctas < off + u.tiles) ++c1;
+  while (c1 + 1 < ctas && total * (c1 + 1) / ctas < off + u.cost()) ++c1;
   // a thread has four dimensions of a row; partials are [tile][D / 4][128 rows][4]
   const int pr = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, x = pr / kRows, row = pr % kRows;
   const int i = x * qpt + row / d.G;
@@ -782,24 +856,34 @@ cudaError_t launch_d(const PagedAttend& a, int grid, cudaStream_t st) {
   cudaError_t e = smem_optin_once(opted, prompt_kernel<D>, C::SMEM);
   if (e != cudaSuccess) return e;
   const int qpt = kRows / a.d.G;
-  prompt_kernel<D><<<grid, kThreads, C::SMEM, st>>>(a, qpt);
+  split_kernel<D><<<dim3(paged_prompt_tiles(a.d.G, a.n_reqs, a.total_q), a.d.Hkv), kRows, 0, st>>>(a, qpt);
   e = cudaGetLastError();
-  if (e != cudaSuccess || grid == 1) return e;
+  if (e != cudaSuccess) return e;
+  // each kernel starts while the one before ends, and waits for its results where it needs them
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid - 1, 2 * kRows / kJoinRows);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  cfg.stream = st;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  e = cudaLaunchKernelEx(&cfg, prompt_kernel<D>, a, qpt);
+  if (e != cudaSuccess || grid == 1) return e;
+  cfg.gridDim = dim3(grid - 1, 2 * kRows / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D>, a, qpt, grid);
 }
 
 }  // namespace
 
 int paged_prompt_rows() { return 2 * kRows; }
+// Tiles of split queries that a call may have.
+int paged_prompt_tiles(int G, int n_reqs, int total_q) { return total_q / (kRows / G) + n_reqs; }
+size_t paged_prompt_tile_bytes(int D) { return (size_t)kRows * 2 * D; }
 
 cudaError_t launch_paged_prompt(const PagedAttend& a, int grid, cudaStream_t st) {
   return a.d.D == 64 ? launch_d<64>(a, grid, st) : launch_d<128>(a, grid, st);
