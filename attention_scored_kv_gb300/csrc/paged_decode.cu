@@ -564,40 +564,61 @@ __device__ __forceinline__ int cta_of(long long x, long long total, int ctas) {
   return (int)(((x + 1) * ctas + total - 1) / total) - 1;
 }
 
-// Adds the partials of the units that a cut splits: a CTA per (unit, row).
+// Adds the partials of the units that a cut splits: a CTA per (unit, row), a thread to a
+// dimension and every (256 / D)th part.
+constexpr int kJoinThreads = 256, kMostParts = 1024;
 template <int D, int RT, bool MASS>
-__global__ void __launch_bounds__(128) join_kernel(const PagedAttend a, const int grid) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttend a, const int grid) {
   __shared__ long long sums[16];
+  __shared__ float weight[kMostParts];
+  __shared__ float acc_of[kJoinThreads];
+  launch_dependents();
   const PagedDev& d = a.d;
   const int unit = blockIdx.x, r = unit / d.Hkv, h = unit % d.Hkv, row = blockIdx.y, tid = threadIdx.x;
   const Unit u = unit_of(a, r);
-  long long total = 1, before = 0;
-  if (u.tiles > 0 && row < u.n * d.G) total_tiles(a, r, 128, sums, total, before);
-  const long long off = before + (long long)h * u.tiles;
-  const int ctas = (int)min((long long)grid, total);
-  const int c0 = cta_of(off, total, ctas), c1 = u.tiles ? cta_of(off + u.tiles - 1, total, ctas) : c0;
+  const bool live = u.tiles > 0 && row < u.n * d.G;
+  int c0 = 0, n = 1;
+  size_t rec0 = 0;
+  if (live) {
+    long long total, before;
+    total_tiles(a, r, kJoinThreads, sums, total, before);
+    const long long off = before + (long long)h * u.tiles;
+    const int ctas = (int)min((long long)grid, total);
+    c0 = cta_of(off, total, ctas);
+    n = cta_of(off + u.tiles - 1, total, ctas) - c0 + 1;
+    rec0 = (size_t)(2 * c0 + (off > total * c0 / ctas ? 1 : 0)) * RT + row;   // the first CTA's: maybe not its first unit
+  }
   wait_previous();
-  if (u.tiles == 0 || row >= u.n * d.G || c0 == c1) return;
-  auto rec_of = [&](int c) {
-    const bool first = off <= total * c / ctas;            // the unit is the CTA's first
-    return (size_t)(2 * c + (first ? 0 : 1)) * RT + row;
-  };
-  float top = -INFINITY;
-  for (int c = c0; c <= c1; ++c) top = fmaxf(top, a.part_ml[rec_of(c)].x);
+  if (!live || n == 1) return;
+  auto rec_of = [&](int i) { return i == 0 ? rec0 : (size_t)(2 * (c0 + i)) * RT + row; };
+  // every warp finds the maximum and the sum; the parts' weights go to shared memory
+  float top = -INFINITY, sum = 0.f;
+  for (int i = tid & 31; i < n; i += 32) top = fmaxf(top, a.part_ml[rec_of(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float ref = top > -INFINITY ? top : 0.f;
-  float sum = 0.f, acc = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const size_t rec = rec_of(c);
-    const float2 ml = a.part_ml[rec];
+  for (int i = tid & 31; i < n; i += 32) {
+    const float2 ml = a.part_ml[rec_of(i)];
     const float f = ex2(ml.x - ref);
     sum = fmaf(ml.y, f, sum);
-    if (tid < D) acc = fmaf(a.part_o[rec * D + tid], f, acc);
+    if (tid < 32) weight[i] = f;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncthreads();
+  float acc = 0.f;
+  const int dim = tid % D;
+#pragma unroll 8
+  for (int i = tid / D; i < n; i += kJoinThreads / D) acc = fmaf(a.part_o[rec_of(i) * D + dim], weight[i], acc);
+  acc_of[tid] = acc;
+  __syncthreads();
   const int hq = h * d.G + row % d.G;
-  if (tid < D)
+  if (tid < D) {
+#pragma unroll
+    for (int k = 1; k < kJoinThreads / D; ++k) acc += acc_of[tid + k * D];
     static_cast<__nv_bfloat16*>(a.out)[((size_t)(u.first + row / d.G) * d.Hq + hq) * D + tid] =
         __float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f);
+  }
   if (MASS && tid == 0) a.lse[(size_t)r * d.Hq + hq] = top + log2f(sum);
 }
 
@@ -607,13 +628,14 @@ cudaError_t launch(const PagedAttend& a, int grid, cudaStream_t st) {
   static std::atomic<unsigned long long> opted{0};
   cudaError_t e = smem_optin_once(opted, decode_kernel<D, RT, MASS>, C::SMEM);
   if (e != cudaSuccess) return e;
+  if (grid > kMostParts) return cudaErrorInvalidConfiguration;
   decode_kernel<D, RT, MASS><<<grid, kThreads, C::SMEM, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int rows = a.max_q_len * a.d.G;
   cfg.gridDim = dim3(a.n_reqs * a.d.Hkv, rows);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -221,22 +221,32 @@ __global__ void __launch_bounds__(kWarps * 32) general_join_kernel(const PagedAt
   if (a.lse && lane == 0) a.lse[(size_t)x.r * d.Hq + hq] = top + log2f(sum);
 }
 
-// Block masses: a warp per (request, block), the query heads over its lanes.  The attend
-// left log2 of each head's weight sum in the block and of its whole sum.
+// Block masses: the query heads over a warp's lanes, four blocks at a time.  The attend left
+// log2 of each head's weight sum in the block and of its whole sum.
+constexpr int kMassBlocks = 16;          // of a warp
 __global__ void __launch_bounds__(kWarps * 32) mass_kernel(const PagedAttend a) {
   const int lane = threadIdx.x & 31, r = blockIdx.x, Hq = a.d.Hq;
   const RowRange x = row_range(a, r);
-  if (!x.live || x.hi <= x.lo) return;
-  const int b1 = (x.hi + kBlock - 1) / kBlock;
-  for (int b = x.lo / kBlock + blockIdx.y * kWarps + (threadIdx.x >> 5); b < b1; b += gridDim.y * kWarps) {
-    float best = 0.f;
+  const int b1 = x.live && x.hi > x.lo ? (x.hi + kBlock - 1) / kBlock : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int first = x.lo / kBlock + (blockIdx.y * kWarps + (threadIdx.x >> 5)) * kMassBlocks;
+  for (int i = 0, c = first; c < b1; ++i) {
+    uint32_t best[4] = {0u, 0u, 0u, 0u};               // of numbers >= 0, whose bits are in their order
     for (int h = lane; h < Hq; h += 32) {
-      const float s = a.blk[((size_t)r * a.table_stride + b) * Hq + h];
-      if (s > -INFINITY) best = fmaxf(best, exp2f(s - a.lse[(size_t)r * Hq + h]));
+      const float lse = a.lse[(size_t)r * Hq + h];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float s = c + k < b1 ? a.blk[((size_t)r * a.table_stride + c + k) * Hq + h] : -INFINITY;
+        if (s > -INFINITY) best[k] = max(best[k], __float_as_uint(exp2f(s - lse)));
+      }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-    if (lane == 0) a.mass[(size_t)r * a.table_stride + b] = best;
+    for (int k = 0; k < 4; ++k) {
+      best[k] = __reduce_max_sync(0xffffffffu, best[k]);
+      if (lane == 0 && c + k < b1) a.mass[(size_t)r * a.table_stride + c + k] = __uint_as_float(best[k]);
+    }
+    c += 4;
+    if ((i + 1) % (kMassBlocks / 4) == 0) c += (gridDim.y * kWarps - 1) * kMassBlocks;   // a grid shorter than the table
   }
 }
 
@@ -265,9 +275,17 @@ cudaError_t launch_paged_general(const PagedAttend& a, cudaStream_t st) {
 }
 
 cudaError_t launch_paged_mass(const PagedAttend& a, cudaStream_t st) {
-  const int ctas = (int)cdiv64(a.table_stride, kWarps * 4);      // four blocks to a warp
-  mass_kernel<<<dim3(a.n_reqs, ctas < 65535 ? ctas : 65535), kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.stream = st;
+  const int64_t ctas = cdiv64(a.table_stride, kWarps * kMassBlocks);
+  cfg.gridDim = dim3(a.n_reqs, (unsigned)(ctas < 65535 ? ctas : 65535));
+  cfg.blockDim = dim3(kWarps * 32);
+  return cudaLaunchKernelEx(&cfg, mass_kernel, a);
 }
 
 }  // namespace kvs

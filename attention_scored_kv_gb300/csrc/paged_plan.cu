@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
   __shared__ Item warp_sums[kThreads / 32];
   __shared__ int s_start[kChunk + 1];      // first row of the request
   __shared__ int s_ctx[kChunk];            // its cached tokens; negative: denied
-  __shared__ int s_page[kChunk];           // pages taken before it
+  __shared__ int s_page[kChunk + 1];       // pages taken before it
   const int tid = threadIdx.x, G = gridDim.x, cta = blockIdx.x;
   const long long most = (long long)a.stride * kBlock;
   const int count = TAKE ? max(0, min(*a.count_in, a.free_capacity)) : 0;
@@ -101,7 +101,10 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
       if (grant && need) taken = max(taken, incl.pages);
       if (!TAKE && !fits && q > 0) err |= kErrCapacity;
     }
-    if (tid == m - 1) s_start[m] = (int)min(incl.rows, (long long)INT32_MAX);
+    if (tid == m - 1) {
+      s_start[m] = (int)min(incl.rows, (long long)INT32_MAX);
+      s_page[m] = (int)min(incl.pages, (long long)INT32_MAX);
+    }
     carry = add(carry, warp_sums[kThreads / 32 - 1]);
     __syncthreads();
     if (TAKE) cluster_wait();
@@ -111,14 +114,17 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
       if (TAKE) a.kv_len[r] = grant ? c + q : c;
     }
     if (TAKE) {
-      // table entries, a warp to a request
-      for (int i = cta * (kThreads / 32) + (tid >> 5); i < m; i += G * (kThreads / 32)) {
+      // table entries, a thread to a page
+      const int pages = s_page[m];
+      for (int j = s_page[0] + cta * kThreads + tid; j < pages; j += G * kThreads) {
+        int i = 0, top = m - 1;
+        while (i < top) {
+          const int mid = (i + top + 1) >> 1;
+          if (s_page[mid] <= j) i = mid; else top = mid - 1;
+        }
         const int ci = s_ctx[i];
-        if (ci < 0) continue;
-        const int qi = s_start[i + 1] - s_start[i], h = (ci + kBlock - 1) / kBlock;
-        const int nb = (ci + qi + kBlock - 1) / kBlock - h;
-        for (int b = tid & 31; b < nb; b += 32)
-          a.table[(size_t)(r0 + i) * a.stride + h + b] = a.free_pages[count - 1 - (s_page[i] + b)];
+        if (ci < 0) continue;                // denied
+        a.table[(size_t)(r0 + i) * a.stride + (ci + kBlock - 1) / kBlock + (j - s_page[i])] = a.free_pages[count - 1 - j];
       }
     }
     // rows, four to a thread
@@ -247,13 +253,17 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const PagedDev d, int
 
 template <bool TAKE>
 cudaError_t launch(const Args& a, int grid, bool cluster, cudaStream_t st) {
+  if (!cluster || grid == 1) {
+    plan_kernel<TAKE><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster ? grid : 1;
+  at[0].val.clusterDim.x = grid;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;

@@ -6,13 +6,15 @@
 // codes c become rn(c * old / s) if s grew, 0 if the page starts.  x / s and c * old / s
 // are products with powers of two, so each value is rounded once, to its code.
 //
-// How: a warp owns one (run, KV head, cache): it reads the run's rows once, keeps them in
-// registers over the maximum and the conversion, and writes whole 16-byte pieces.  K
+// How: a warp owns one (run, KV head, cache): it reads the run's rows once, keeps them as
+// they came over the maximum and the conversion, and writes whole 16-byte pieces.  K
 // pieces are 16 dimensions of a token; V pieces are 16 tokens of a dimension, so for V a
-// lane reads four dimensions of each token (whole rows stay coalesced) and the
-// transposition costs no shared memory.  The row that starts a run leads it; others exit,
-// so a batch of single tokens is one warp per token and cache, and rows of a long prompt
-// are taken sixteen to a warp to spare idle warps.
+// lane reads four dimensions of each token (whole rows stay coalesced) and the pieces
+// pass through shared memory once, to leave in order.  The maximum is taken over the bits
+// of |x|, two bf16 at a time, which also shows whether an infinity or a NaN is there; only
+// then are values looked at one by one.  The row that starts a run leads it; others exit, so
+// a batch of single tokens is one warp per token and cache, and rows of a long prompt are
+// taken sixteen to a warp to spare idle warps.
 #include "append_store.cuh"
 #include "paged.cuh"
 
@@ -21,18 +23,64 @@ namespace {
 
 constexpr int kWarps = 4;
 
-template <int IN>
-__device__ __forceinline__ void load4(const void* base, size_t elem, float v[4]) {
-  if constexpr (IN == KVS_BF16) {
-    const uint2 raw = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + elem);
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.y));
-    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-  } else {
-    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+// N consecutive inputs as they are in memory.
+template <int IN, int N>
+struct Raw {
+  static constexpr bool B = IN == KVS_BF16;
+  static constexpr int W = B ? N / 2 : N;
+  uint32_t w[W];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0;
   }
+  __device__ __forceinline__ void load(const void* base, size_t elem) {
+    const char* p = static_cast<const char*>(base) + elem * (B ? 2 : 4);
+    if constexpr (W % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+        w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+      }
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x; w[1] = v.y;
+    }
+  }
+  // The largest |x| as bits: of float32, or of two bf16 in halves.
+  __device__ __forceinline__ uint32_t top(uint32_t so_far) const {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      so_far = B ? __vmaxu2(so_far, w[i] & 0x7fff7fffu) : max(so_far, w[i] & 0x7fffffffu);
+    return so_far;
+  }
+  // The same without what is not finite; NaN becomes 0.
+  __device__ __forceinline__ uint32_t clean(uint32_t so_far, bool& nan) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if constexpr (B) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 16) {
+          const uint32_t a = w[i] >> k & 0x7fffu;
+          if (a > 0x7f80u) { nan = true; w[i] &= ~(0xffffu << k); }
+          if (a < 0x7f80u) so_far = __vmaxu2(so_far, a);
+        }
+      } else {
+        const uint32_t a = w[i] & 0x7fffffffu;
+        if (a > 0x7f800000u) { nan = true; w[i] = 0; }
+        if (a < 0x7f800000u) so_far = max(so_far, a);
+      }
+    }
+    return so_far;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return B ? __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) : __uint_as_float(w[i]);
+  }
+};
+template <int IN>
+__device__ __forceinline__ float bits_to_float(uint32_t top) {
+  return IN == KVS_BF16 ? __uint_as_float(max(top << 16, top & 0xffff0000u)) : __uint_as_float(top);
 }
+__device__ __forceinline__ bool is_finite(float v) { return __float_as_uint(v) < 0x7f800000u; }
 
 template <int OUT>
 __device__ __forceinline__ void store4(void* base, size_t elem, const float v[4]) {
@@ -47,23 +95,14 @@ __device__ __forceinline__ void store4(void* base, size_t elem, const float v[4]
   }
 }
 
-// A value as it takes part in the scale: NaN becomes 0, an infinity stays out of the maximum.
-__device__ __forceinline__ float clean(float x, float& amax, bool& nan) {
-  if (x != x) { nan = true; return 0.f; }
-  const float a = fabsf(x);
-  if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
-  return x;
-}
-
 __device__ __forceinline__ uint32_t requantise4(uint32_t codes, float ratio) {
   const float2 a = e4m3x2_to_float2(codes & 0xffffu), b = e4m3x2_to_float2(codes >> 16);
   return float2_to_e4m3x2(a.x * ratio, a.y * ratio) | (float2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
 }
 
+// The warp's largest |x|, and whether any lane has one that is not finite.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
 // A run: rows of one page, at most 16.  Lane t < 16 holds the row of slot t in the page (-1: none).
@@ -81,26 +120,26 @@ __device__ void store_k(const PagedDev& d, int layer, int head, const void* x, c
   float* scale_at = &d.scales[layer * d.layer_scales + at].x;
   const bool fresh = run.have & 1;
   const float old = fresh ? exp2_int(kScaleMinExp) : fmaxf(*scale_at, exp2_int(kScaleMinExp));
-  float v[NP][16];
-  float amax = 0.f;
-  bool nan = false;
+  Raw<IN, 16> v[NP];
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int piece = i * 32 + lane, t = piece / CH, c = piece % CH;
     const int row = __shfl_sync(0xffffffffu, run.row, t & 15);
-    if (piece >= 16 * CH || row < 0) continue;
-    const size_t e = ((size_t)row * d.Hkv + head) * D + c * 16;
-    load8<IN>(x, e, v[i]);
-    load8<IN>(x, e + 8, v[i] + 8);
+    if (piece < 16 * CH && row >= 0) v[i].load(x, ((size_t)row * d.Hkv + head) * D + c * 16);
+    else v[i].zero();
   }
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int piece = i * 32 + lane, t = piece / CH;
-    if (piece >= 16 * CH || !(run.have >> t & 1)) continue;
+  for (int i = 0; i < NP; ++i) top = v[i].top(top);
+  float amax = warp_max(bits_to_float<IN>(top));
+  if (!is_finite(amax)) {
+    bool nan = false;
+    top = 0;
 #pragma unroll
-    for (int u = 0; u < 16; ++u) v[i][u] = clean(v[i][u], amax, nan);
+    for (int i = 0; i < NP; ++i) top = v[i].clean(top, nan);
+    amax = warp_max(bits_to_float<IN>(top));
+    if (nan) paged_error(d, kErrState);
   }
-  amax = warp_max(amax);
   const float scale = fmaxf(old, exp2_int(scale_exp(amax)));
   const float inv = 1.f / scale, ratio = old * inv;      // powers of two: exact
 #pragma unroll
@@ -113,8 +152,8 @@ __device__ void store_k(const PagedDev& d, int layer, int head, const void* x, c
       uint32_t* p = &w.x;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        p[u] = float2_to_e4m3x2(v[i][4 * u] * inv, v[i][4 * u + 1] * inv) |
-               (float2_to_e4m3x2(v[i][4 * u + 2] * inv, v[i][4 * u + 3] * inv) << 16);
+        p[u] = float2_to_e4m3x2(v[i].at(4 * u) * inv, v[i].at(4 * u + 1) * inv) |
+               (float2_to_e4m3x2(v[i].at(4 * u + 2) * inv, v[i].at(4 * u + 3) * inv) << 16);
     } else if (!fresh) {
       if (ratio == 1.f) continue;
       w = *dst;
@@ -125,39 +164,45 @@ __device__ void store_k(const PagedDev& d, int layer, int head, const void* x, c
   }
   __syncwarp();                                    // every lane has read the old scale
   if (lane == 0) *scale_at = scale;
-  if (nan) paged_error(d, kErrState);
 }
 
+// stage: 16 * D bytes of the warp's shared memory.
 template <int IN, int D>
-__device__ void store_v(const PagedDev& d, int layer, int head, const void* x, const Run& run, int lane) {
+__device__ void store_v(const PagedDev& d, int layer, int head, const void* x, const Run& run, int lane,
+                        uint4* stage) {
   const size_t at = (size_t)run.page * d.Hkv + head;
   uint8_t* base = d.v + layer * d.layer_bytes + at * (16 * D);
   float* scale_at = &d.scales[layer * d.layer_scales + at].y;
   const bool fresh = run.have & 1, mine = lane < D / 4;
   const float old = fresh ? exp2_int(kScaleMinExp) : fmaxf(*scale_at, exp2_int(kScaleMinExp));
-  float v[16][4];
-  float amax = 0.f;
-  bool nan = false;
+  Raw<IN, 4> v[16];
+  uint32_t top = 0;
 #pragma unroll
   for (int t = 0; t < 16; ++t) {
     const int row = __shfl_sync(0xffffffffu, run.row, t);
-    v[t][0] = v[t][1] = v[t][2] = v[t][3] = 0.f;
-    if (row >= 0 && mine) load4<IN>(x, ((size_t)row * d.Hkv + head) * D + lane * 4, v[t]);
+    if (row >= 0 && mine) v[t].load(x, ((size_t)row * d.Hkv + head) * D + lane * 4);
+    else v[t].zero();
   }
 #pragma unroll
-  for (int t = 0; t < 16; ++t)
+  for (int t = 0; t < 16; ++t) top = v[t].top(top);
+  float amax = warp_max(bits_to_float<IN>(top));
+  if (!is_finite(amax)) {
+    bool nan = false;
+    top = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[t][u] = clean(v[t][u], amax, nan);
-  amax = warp_max(amax);
+    for (int t = 0; t < 16; ++t) top = v[t].clean(top, nan);
+    amax = warp_max(bits_to_float<IN>(top));
+    if (nan) paged_error(d, kErrState);
+  }
   const float scale = fmaxf(old, exp2_int(scale_exp(amax)));
   const float inv = 1.f / scale, ratio = old * inv;
+  __syncwarp();                                    // the stage's last use, and the old scale's reads
   if (mine) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      uint4* dst = reinterpret_cast<uint4*>(base + (lane * 4 + u) * 16);
       uint4 w = make_uint4(0, 0, 0, 0);
       if (!fresh && run.have != 0xffffu) {
-        w = *dst;
+        w = reinterpret_cast<const uint4*>(base)[lane * 4 + u];
         if (ratio != 1.f) {
           w.x = requantise4(w.x, ratio); w.y = requantise4(w.y, ratio);
           w.z = requantise4(w.z, ratio); w.w = requantise4(w.w, ratio);
@@ -166,19 +211,23 @@ __device__ void store_v(const PagedDev& d, int layer, int head, const void* x, c
       uint32_t* p = &w.x;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t codes = float2_to_e4m3x2(v[4 * j][u] * inv, v[4 * j + 1][u] * inv) |
-                               (float2_to_e4m3x2(v[4 * j + 2][u] * inv, v[4 * j + 3][u] * inv) << 16);
+        const uint32_t codes = float2_to_e4m3x2(v[4 * j].at(u) * inv, v[4 * j + 1].at(u) * inv) |
+                               (float2_to_e4m3x2(v[4 * j + 2].at(u) * inv, v[4 * j + 3].at(u) * inv) << 16);
         const uint32_t h = run.have >> (4 * j);
         const uint32_t mask = (h & 1 ? 0xffu : 0) | (h & 2 ? 0xff00u : 0) | (h & 4 ? 0xff0000u : 0) |
                               (h & 8 ? 0xff000000u : 0);
         p[j] = (p[j] & ~mask) | (codes & mask);
       }
-      *dst = w;
+      stage[lane * 4 + (u ^ (lane >> 1 & 3))] = w;         // spread over the banks
     }
   }
   __syncwarp();
+#pragma unroll
+  for (int i = 0; i < (D + 31) / 32; ++i) {
+    const int q = i * 32 + lane, from = q / 4;
+    if (q < D) reinterpret_cast<uint4*>(base)[from * 4 + ((q & 3) ^ (from >> 1 & 3))] = stage[q];
+  }
   if (lane == 0) *scale_at = scale;
-  if (nan) paged_error(d, kErrState);
 }
 
 // grid: x groups of `per` rows, kWarps to a CTA; y KV heads; z 0 = K, 1 = V.
@@ -186,6 +235,7 @@ template <int IN, int D>
 __global__ void __launch_bounds__(kWarps * 32) append_kernel(const PagedDev d, int layer, int n_rows, int per,
                                                              const int32_t* __restrict__ slots, const void* k,
                                                              const void* v) {
+  __shared__ uint4 stage[kWarps][D];
   const int lane = threadIdx.x & 31, head = blockIdx.y;
   const long long first = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * per;
   for (int i = (int)first; i < n_rows && i < first + per; ++i) {
@@ -214,7 +264,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const PagedDev d, i
       }
     }
     if (blockIdx.z == 0) store_k<IN, D>(d, layer, head, k, run, lane);
-    else store_v<IN, D>(d, layer, head, v, run, lane);
+    else store_v<IN, D>(d, layer, head, v, run, lane, stage[threadIdx.x >> 5]);
     i += len - 1;
   }
 }
@@ -257,6 +307,53 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const PagedDev d, i
     return;
   }
   const bool mine = lane < D / 4;
+  const uint8_t* vbase = d.v + layer * d.layer_bytes;
+  // Rows in page order, which may pass into another page: the usual case, of whole contexts.  Both pages'
+  // bytes are then shifted into row order at once.
+  const int s0 = __shfl_sync(0xffffffffu, s, 0), off = s0 & 15, cut = 16 - off;
+  const int s1 = __shfl_sync(0xffffffffu, s, cut & 15);
+  const bool in_order = lane >= n || s == (lane < cut ? s0 + lane : s1 + lane - cut);
+  const bool two = off > 0 && cut < n;
+  if (s0 >= 0 && per == 16 && __all_sync(0xffffffffu, in_order) && (!two || (s1 >= 0 && (s1 & 15) == 0))) {
+    const float sa = __shfl_sync(0xffffffffu, sc.y, 0), sb = __shfl_sync(0xffffffffu, sc.y, cut & 15);
+    if (!mine) return;
+    const uint4* pa = reinterpret_cast<const uint4*>(vbase + ((size_t)(s0 >> 4) * d.Hkv + head) * (16 * D)) + lane * 4;
+    const uint4* pb = reinterpret_cast<const uint4*>(vbase + ((size_t)((two ? s1 : s0) >> 4) * d.Hkv + head) * (16 * D)) + lane * 4;
+    uint32_t c[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint4 x = __ldg(pa + u), y = two ? __ldg(pb + u) : make_uint4(0, 0, 0, 0);
+      c[u][0] = x.x; c[u][1] = x.y; c[u][2] = x.z; c[u][3] = x.w;
+      c[u][4] = y.x; c[u][5] = y.y; c[u][6] = y.z; c[u][7] = y.w;
+    }
+    const int words = off >> 2, bits = (off & 3) * 8;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < words) {
+#pragma unroll
+          for (int i = 0; i < 7; ++i) c[u][i] = c[u][i + 1];
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[u][i] = __funnelshift_r(c[u][i], c[u][i + 1], bits);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      float2 f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) f[u] = e4m3x2_to_float2(c[u][j / 4] >> (j & 2 ? 16 : 0) & 0xffffu);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (j + k < n) {
+          const float scale = j + k < cut ? sa : sb;
+          const float o[4] = {(k ? f[0].y : f[0].x) * scale, (k ? f[1].y : f[1].x) * scale,
+                              (k ? f[2].y : f[2].x) * scale, (k ? f[3].y : f[3].x) * scale};
+          store4<OUT>(v, ((size_t)(i0 + j + k) * d.Hkv + head) * D + lane * 4, o);
+        }
+    }
+    return;
+  }
   int page = -2;
   uint4 w[4];
   for (int j = 0; j < n; ++j) {

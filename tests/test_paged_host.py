@@ -75,6 +75,7 @@ def test_null_handles_are_refused():
 def test_binding_refuses_host_tensors():
     cache = object.__new__(kvs.PagedCache)
     cache.cfg, cache.device, cache.in_dtype = cfg(), torch.device("cuda", 0), torch.bfloat16
+    cache._index, cache._row, cache._qrow = 0, (4, 128), (32, 128)
     ints = torch.zeros(4, dtype=torch.int32)
     kv = torch.zeros((4, 4, 128), dtype=torch.bfloat16)
     for call in (lambda: cache.append(0, kv, kv, ints), lambda: cache.gather(0, ints),
