@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
   w.clip();
 
   if (warp == 4) {
-    // ---- copies: lane j < 8 has block j of the tile
+    // ---- copies.  The table entries and scales of four tiles are loaded at once, a lane to a block, and
+    // those of the next four while these are copied: their two latencies in a row took longer than a tile.
     const uint64_t policy = evict_first_policy();
     const uint8_t* kbase = d.k + a.layer * d.layer_bytes;
     const uint8_t* vbase = d.v + a.layer * d.layer_bytes;
@@ -238,30 +239,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
     bool ok = true;
     while (w.left > 0 && ok) {
       const int32_t* row = a.table + (size_t)w.r * a.table_stride;
-      auto fetch = [&](int t, int& nb, int& page, float2& sc) {
-        const int b = w.u.b0 + t * kTileBlocks;
-        nb = max(0, min(kTileBlocks, w.u.b0 + w.u.nb - b));
-        page = -1;
-        sc = make_float2(0.f, 1.f);
-        if (lane < nb) {
-          page = __ldg(row + b + lane);
-          if (page < 0 || page >= d.num_pages) {
-            paged_error(d, kErrState);
-            page = 0;
-          } else {
-            sc = __ldg(sbase + (size_t)page * d.Hkv + w.h);
-            sc.x = fmaxf(sc.x, exp2_int(kScaleMinExp));      // a page that nothing was stored in has 0
-            sc.y = fmaxf(sc.y, exp2_int(kScaleMinExp));
-          }
-        }
+      const int stop = w.u.b0 + w.u.nb;
+      auto load_page = [&](int t) {                         // of the lane's block from tile t on
+        const int b = w.u.b0 + t * kTileBlocks + lane;
+        return t < w.t0 + w.nt && b < stop ? __ldg(row + b) : -1;
       };
-      int nb, page;
-      float2 sc;
-      fetch(w.t0, nb, page, sc);
+      auto load_scale = [&](int page) {
+        return page >= 0 && page < d.num_pages ? __ldg(sbase + (size_t)page * d.Hkv + w.h) : make_float2(0.f, 1.f);
+      };
+      int page = load_page(w.t0), page_next = load_page(w.t0 + 4);
+      float2 sc = load_scale(page), sc_next = make_float2(0.f, 1.f);
       for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
+        const int four = (t - w.t0) & 3, nb = max(0, min(kTileBlocks, w.u.nb - t * kTileBlocks));
+        if (four == 0 && t > w.t0) {
+          page = page_next;
+          sc = sc_next;
+          page_next = load_page(t + 4);
+        }
         const int st = count % C::NS;
-        if (count >= C::NS) ok = mbar_wait(smem_u32(&ms.empty[st]), (count / C::NS - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
+        if (count >= C::NS) ok = warp_wait(smem_u32(&ms.empty[st]), (count / C::NS - 1) & 1);
         if (!ok) break;
         const uint32_t full = smem_u32(&ms.full[st]);
         const uint32_t dst = smem_u32(ring + st * C::STAGE);
@@ -270,23 +266,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
         const int odd = nb & 1;
         if (lane == 0) mbar_expect(full, (2 * nb + odd) * C::PAGE);
         __syncwarp();
-        const int page0 = __shfl_sync(0xffffffffu, page, 0);
-        if (lane < nb) {
-          const size_t at = ((size_t)page * d.Hkv + w.h) * C::PAGE;
-          bulk_load(dst + lane * C::PAGE, kbase + at, C::PAGE, full, policy);
-          bulk_load(dst + C::HALF + lane * C::PAGE, vbase + at, C::PAGE, full, policy);
-        } else if (lane == nb && odd) {
-          bulk_load(dst + C::HALF + lane * C::PAGE, vbase + ((size_t)page0 * d.Hkv + w.h) * C::PAGE, C::PAGE, full, policy);
-        }
+        const int of = four * kTileBlocks + (lane < nb ? lane : 0);
+        const int mine = __shfl_sync(0xffffffffu, page, of);
+        const bool good = mine >= 0 && mine < d.num_pages;
+        const size_t at = ((size_t)(good ? mine : 0) * d.Hkv + w.h) * C::PAGE;
+        if (lane < nb) bulk_load(dst + lane * C::PAGE, kbase + at, C::PAGE, full, policy);
+        if (lane < nb + odd) bulk_load(dst + C::HALF + lane * C::PAGE, vbase + at, C::PAGE, full, policy);
+        const float ks = __shfl_sync(0xffffffffu, sc.x, of), vs = __shfl_sync(0xffffffffu, sc.y, of);
         if (lane < kTileBlocks) {
-          const float ev = (float)((__float_as_int(sc.y) >> 23) - 127);
-          ms.ks[st][lane] = sc.x;                           // 0: nothing of this block is visible
+          const bool seen = lane < nb && good;
+          if (lane < nb && !good) paged_error(d, kErrState);
+          const float v = seen ? fmaxf(vs, exp2_int(kScaleMinExp)) : 1.f;      // a page that nothing was stored in has 0
+          const float ev = (float)((__float_as_int(v) >> 23) - 127);
+          ms.ks[st][lane] = seen ? fmaxf(ks, exp2_int(kScaleMinExp)) : 0.f;    // 0: nothing of this block is visible
           ms.ev[st][lane] = ev;
           ms.iv[st][lane] = exp2_int(-(int)ev);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
-        if (t + 1 < w.t0 + w.nt) fetch(t + 1, nb, page, sc);
+        if (four == 0) sc_next = load_scale(page_next);
       }
       if (ok) w.next(a);
     }
