@@ -163,40 +163,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
 
   launch_dependents();
   if (blockIdx.x == 0) report_rows(a, kThreads);
-  // this CTA's range
-  long long total, unused;
-  total_tiles(a, 0, kThreads, ms.sums, total, unused);
-  const long long ctas = min((long long)gridDim.x, total);      // every one of them has a tile
-  if (blockIdx.x >= ctas) return;
-  const long long begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
-  // where it begins: the request whose units hold tile `begin`
-  {
-    long long at = 0;
-    for (int r0 = 0; r0 < a.n_reqs; r0 += kThreads) {
-      const int r = r0 + tid;
-      const int tiles = r < a.n_reqs ? unit_of(a, r).tiles : 0;
-      long long mine = (long long)tiles * d.Hkv, upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-      }
-      if (lane == 31) ms.sums[warp] = upto;
-      __syncthreads();
-      long long base = at;
-      for (int w = 0; w < warp; ++w) base += ms.sums[w];
-      for (int w = 0; w < kThreads / 32; ++w) at += ms.sums[w];
-      upto += base;
-      if (begin >= upto - mine && begin < upto) {
-        const int off = (int)(begin - (upto - mine));
-        ms.start_r = r;
-        ms.start_h = off / tiles;
-        ms.start_t = off % tiles;
-      }
-      __syncthreads();
-      if (at > begin) break;
-    }
-  }
+  // barriers and TMEM while the lengths load
+  Unit mine_u = unit_of(a, min(tid, a.n_reqs - 1));
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(smem_u32(&ms.full[i]), 1);
@@ -215,9 +183,54 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
     umma::alloc(smem_u32(&ms.tmem), C::TMEM);
     umma::relinquish();
   }
+  // this CTA's range: kThreads requests at a time (a call of more has their tiles counted first)
+  long long total = 0, base = 0;
+  if (a.n_reqs > kThreads) {
+    long long unused;
+    total_tiles(a, 0, kThreads, ms.sums, total, unused);
+  }
+  long long begin = 0, end = 0;
+  for (int r0 = 0; r0 < a.n_reqs; r0 += kThreads) {
+    const int r = r0 + tid;
+    if (r0 > 0) mine_u = unit_of(a, min(r, a.n_reqs - 1));
+    const int tiles = r < a.n_reqs ? mine_u.tiles : 0;
+    const long long mine = (long long)tiles * d.Hkv;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) ms.sums[warp] = upto;
+    __syncthreads();
+    long long all = base;
+    upto += base;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) upto += ms.sums[i];
+      all += ms.sums[i];
+    }
+    if (a.n_reqs <= kThreads) total = all;
+    const long long ctas = min((long long)gridDim.x, total);      // every one of them has a tile
+    begin = ctas > blockIdx.x ? total * blockIdx.x / ctas : total;
+    end = ctas > blockIdx.x ? total * (blockIdx.x + 1) / ctas : total;
+    if (begin >= upto - mine && begin < upto) {
+      const int off = (int)(begin - (upto - mine));
+      ms.start_r = r;
+      ms.start_h = off / tiles;
+      ms.start_t = off % tiles;
+    }
+    __syncthreads();
+    base = all;
+    if (all > begin) break;
+  }
   umma::fence_before();
   __syncthreads();
   umma::fence_after();
+  if (begin >= end) {                        // more CTAs than tiles
+    if (warp == 5) umma::dealloc(ms.tmem, C::TMEM);
+    return;
+  }
   const uint32_t tmem = ms.tmem, t_o = tmem + 2 * N;
   Walk w;
   w.r = ms.start_r;

@@ -36,7 +36,7 @@ constexpr int kThreads = 512;            // 8 softmax warps, K copies, matrix, q
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10, kVWarp = 12, kVThreads = 128;
 // Registers of a softmax thread and of the others: 256 (168 + 88) = the block's 65536.
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
-constexpr int kKStages = 3, kVStages = 1, kQStages = 2;
+constexpr int kKStages = 3, kVStages = 2, kQStages = 1;
 constexpr int kSlots = 4;                // scales of this many tiles, row factors of this many segments
 constexpr int kSetup = 2;                // what a unit's start costs, in tiles, where work is cut
 constexpr int kRows = 128;               // rows of a tile of queries
