@@ -46,6 +46,7 @@ struct PagedAttend {
   int32_t splits;          // general kernel: parts of a row's range
   uint8_t* q_pieces;       // prompt kernel: split queries, and their rows' factors
   float* q_factors;
+  int32_t* cuts;           // prompt kernel: 8 words a CTA
 };
 
 // How a call runs: a pure function of host-known sizes, so that the scratch size and the
@@ -55,7 +56,7 @@ struct PagedAttendPlan {
   int splits;              // general kernel
   int rows;                // decode kernel: query rows of a unit
   int grid;                // decode and prompt kernels
-  size_t part_o, part_ml, blk, lse, q_pieces, q_factors, total;   // scratch offsets
+  size_t part_o, part_ml, blk, lse, q_pieces, q_factors, cuts, total;   // scratch offsets
 };
 
 __host__ __device__ inline size_t k_code(int D, int t, int d) {

@@ -146,7 +146,8 @@ PagedAttendPlan plan_attend(const kvs_paged* pc, int n_reqs, int stride, int tot
   p.q_pieces = p.lse + (mass ? up((size_t)n_reqs * d.Hq * sizeof(float)) : 0);
   const size_t tiles = p.kernel == PagedAttendPlan::kPrompt ? (size_t)paged_prompt_tiles(d.G, n_reqs, total_q) * d.Hkv : 0;
   p.q_factors = p.q_pieces + up(tiles * paged_prompt_tile_bytes(d.D));
-  p.total = p.q_factors + up(tiles * (paged_prompt_rows() / 2) * sizeof(float));
+  p.cuts = p.q_factors + up(tiles * (paged_prompt_rows() / 2) * sizeof(float));
+  p.total = p.cuts + (p.kernel == PagedAttendPlan::kPrompt ? up((size_t)p.grid * 32) : 0);
   return p;
 }
 
@@ -368,6 +369,7 @@ kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const 
   a.splits = p.splits;
   a.q_pieces = s + p.q_pieces;
   a.q_factors = reinterpret_cast<float*>(s + p.q_factors);
+  a.cuts = reinterpret_cast<int32_t*>(s + p.cuts);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = p.kernel == PagedAttendPlan::kDecode   ? launch_paged_decode(a, p.rows, p.grid, cs)
                   : p.kernel == PagedAttendPlan::kPrompt ? launch_paged_prompt(a, p.grid, cs)

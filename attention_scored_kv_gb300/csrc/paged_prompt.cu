@@ -224,6 +224,12 @@ struct Walk {
   }
 };
 
+// The unit that CTA c's share enters in its middle, if that is the unit's first cut: the unit and the CTAs
+// [c - 1, last] that have a part of it.  The CTA before is in its slot 1 unless the unit is its first.
+struct Cut {
+  int r, qg, h, last, slot;                // last 0: none
+};
+
 struct Misc {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], drain;
   uint64_t s_ready[2], p_ready[2], o_done[2];
@@ -406,9 +412,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
   if (blockIdx.x == 0) report_rows(a, kThreads);
   const long long total = total_tiles(a, per, kThreads / 32, search);
   const long long ctas = min((long long)gridDim.x, total);
-  if (blockIdx.x >= ctas) return;
+  if (blockIdx.x >= ctas) {
+    if (tid == 0) a.cuts[blockIdx.x * 8 + 3] = 0;
+    return;
+  }
   const long long begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
   locate(a, per, kThreads / 32, begin, search);
+  if (tid == 0) {
+    const int c = blockIdx.x;
+    const long long off = begin - search.t;               // the unit's start
+    Cut cut{search.r, search.qg, search.h, 0, 0};
+    if (search.t > kSetup && total * (c - 1) / ctas <= off + kSetup) {
+      const Unit u = unit_of(a, req_of(a, cut.r), cut.qg, per);
+      cut.last = c;
+      while (cut.last + 1 < ctas && total * (cut.last + 1) / ctas < off + u.cost()) ++cut.last;
+      cut.slot = off > total * (c - 1) / ctas;
+    }
+    int* at = a.cuts + c * 8;
+    at[0] = cut.r; at[1] = cut.qg; at[2] = cut.h; at[3] = cut.last; at[4] = cut.slot;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
@@ -695,9 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
         umma::fence_after();
         uint32_t h[64];
         float f = 1.f, add, big;
-        // Within a segment the last maximum mostly serves: the exponentials are taken at once, and
-        // again only if a block's sum passes what the slack allows (or overflows).
-        bool look = t == 0 || __any_sync(0xffffffffu, m == -INFINITY);
+        // Within a segment the last maximum mostly serves, so the exponentials are taken at once.  Where a
+        // block's sum passes what the slack allows, the row's maximum moves up by log2 of it (at most 4 too
+        // far) and they are taken again; only where even that overflowed are the maxima looked at.
+        bool look = t == 0 || __any_sync(0xffffffffu, m == -INFINITY), last = look;
         for (;;) {
           if (look) {
             const float top = masked ? row_max<true>(t_s, y, c) : row_max<false>(t_s, y, c);
@@ -708,19 +731,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
           }
           const float ref = (m == -INFINITY ? 0.f : m) - kTop;
           add = masked ? row_exp<true>(t_s, y, c, ref, h, big) : row_exp<false>(t_s, y, c, ref, h, big);
-          if (look || !__any_sync(0xffffffffu, !(big <= kLimit))) break;
-          look = true;
+          if (last || !__any_sync(0xffffffffu, !(big <= kLimit))) break;
+          last = true;
+          look = __any_sync(0xffffffffu, !(big < 1e38f));
+          if (!look && big > kLimit) {
+            const float up = __log2f(big);
+            f = ex2(-up);
+            m += up;
+          }
         }
         l = fmaf(l, f, add);
         // S was issued behind the previous product, so that is done with P and O
         if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-          for (int j = 0; j < D; j += 16) {
-            float o[16];
-            ld16(t_o + j, o);
+          for (int j = 0; j < D; j += 32) {
+            float o[32];
+            umma::ld32(t_o + j, o);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] *= f;
-            st16(t_o + j, o);
+            for (int k = 0; k < 32; ++k) o[k] *= f;
+            st32(t_o + j, reinterpret_cast<const uint32_t*>(o));
           }
         }
         st32(t_s, h);                                     // P over S, two tokens to a column
@@ -782,39 +811,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
   }
 }
 
-// Adds the partials of the unit that CTA boundary blockIdx.x + 1 cuts, if that is the unit's first cut.
-constexpr int kJoinThreads = 128, kJoinRows = 8;
+// Adds the partials of the unit that CTA blockIdx.x + 1 left in its cut.
+constexpr int kJoinThreads = 256, kJoinRows = 16;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAttend a, const int qpt,
-                                                                   const int grid) {
-  __shared__ Search search;
-  const PagedDev& d = a.d;
-  const int per = 2 * qpt, c = blockIdx.x + 1;
-  const long long total = total_tiles(a, per, kJoinThreads / 32, search);
-  const int ctas = (int)min((long long)grid, total);
-  bool work = c < ctas;
-  long long off = 0;
-  if (work) {
-    const long long begin = total * c / ctas;
-    locate(a, per, kJoinThreads / 32, begin, search);
-    off = begin - search.t;                               // the unit's start
-    work = search.t > kSetup && total * (c - 1) / ctas <= off + kSetup;
-  }
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAttend a, const int qpt) {
   wait_previous();
-  if (!work) return;
-  const Req q = req_of(a, search.r);
-  const Unit u = unit_of(a, q, search.qg, per);
-  const int c0 = c - 1;
-  int c1 = c;
-  while (c1 + 1 < ctas && total * (c1 + 1) / ctas < off + u.cost()) ++c1;
+  const PagedDev& d = a.d;
+  const int* at = a.cuts + (blockIdx.x + 1) * 8;
+  const int c0 = blockIdx.x, c1 = at[3], r = at[0], qg = at[1], h = at[2], slot = at[4];
+  if (c1 == 0) return;
+  const Req q = req_of(a, r);
+  const Unit u = unit_of(a, q, qg, 2 * qpt);
   // a thread has four dimensions of a row; partials are [tile][D / 4][128 rows][4]
   const int pr = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, x = pr / kRows, row = pr % kRows;
   const int i = x * qpt + row / d.G;
   if (row / d.G >= qpt || i >= u.cnt) return;
-  auto rec_of = [&](int e) {
-    const bool first = off <= total * e / ctas;           // the unit is the CTA's first
-    return ((size_t)(2 * e + (first ? 0 : 1)) * 2 + x) * kRows;
-  };
+  auto rec_of = [&](int e) { return ((size_t)(2 * e + (e == c0 ? slot : 0)) * 2 + x) * kRows; };
   float top = -INFINITY, sum = 0.f;
   for (int e = c0; e <= c1; ++e) top = fmaxf(top, a.part_ml[rec_of(e) + row].x);
   const float ref = top > -INFINITY ? top : 0.f;
@@ -837,7 +849,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAt
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                       ((size_t)(q.first + u.i0 + i) * d.Hq + search.h * d.G + row % d.G) * D;
+                       ((size_t)(q.first + u.i0 + i) * d.Hq + h * d.G + row % d.G) * D;
 #pragma unroll
   for (int q4 = 0; q4 < D / 64; ++q4) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[q4].x * inv, acc[q4].y * inv);
@@ -875,7 +887,7 @@ cudaError_t launch_d(const PagedAttend& a, int grid, cudaStream_t st) {
   cfg.gridDim = dim3(grid - 1, 2 * kRows / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D>, a, qpt, grid);
+  return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D>, a, qpt);
 }
 
 }  // namespace
