@@ -238,21 +238,22 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const PagedDev d, i
   __shared__ uint4 stage[kWarps][D];
   const int lane = threadIdx.x & 31, head = blockIdx.y;
   const long long first = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * per;
-  for (int i = (int)first; i < n_rows && i < first + per; ++i) {
-    const int lead = __ldg(slots + i);
-    if (lead < 0) continue;
-    const int page = lead >> 4;
-    if (i > 0) {
-      const int before = __ldg(slots + i - 1);
-      if (before >= 0 && (before >> 4) == page) continue;
-    }
+  if (first >= n_rows) return;
+  // Lane l has the slot of row first - 1 + l: the row before, the warp's rows and what their runs may reach.
+  const long long mine = first - 1 + lane;
+  const int sl = mine >= 0 && mine < n_rows ? __ldg(slots + mine) : -1;
+  const int before = __shfl_up_sync(0xffffffffu, sl, 1);
+  const bool leads = lane >= 1 && lane <= per && sl >= 0 && !(before >= 0 && before >> 4 == sl >> 4);
+  for (uint32_t todo = __ballot_sync(0xffffffffu, leads); todo; todo &= todo - 1) {
+    const int l = __ffs(todo) - 1, i = (int)first - 1 + l;
+    const int page = __shfl_sync(0xffffffffu, sl, l) >> 4;
     if (page >= d.num_pages) {
       if (lane == 0) paged_error(d, kErrState);
       continue;
     }
     // the run: rows i, i + 1, ... while they stay in the page
-    const int s = lane < 16 && i + lane < n_rows ? __ldg(slots + i + lane) : -1;
-    const uint32_t in = __ballot_sync(0xffffffffu, s >= 0 && (s >> 4) == page);
+    const int s = __shfl_sync(0xffffffffu, sl, (l + lane) & 31);
+    const uint32_t in = __ballot_sync(0xffffffffu, lane < 16 && l + lane < 32 && s >= 0 && s >> 4 == page);
     const int len = __ffs(~in) - 1;
     Run run{page, -1, 0};
 #pragma unroll
@@ -265,7 +266,6 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const PagedDev d, i
     }
     if (blockIdx.z == 0) store_k<IN, D>(d, layer, head, k, run, lane);
     else store_v<IN, D>(d, layer, head, v, run, lane, stage[threadIdx.x >> 5]);
-    i += len - 1;
   }
 }
 
@@ -273,7 +273,6 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const PagedDev d, i
 template <int OUT, int D>
 __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const PagedDev d, int layer, int n_rows, int per,
                                                              const int32_t* __restrict__ slots, void* k, void* v) {
-  constexpr int CH = D / 16, NP = (16 * CH + 31) / 32;
   const int lane = threadIdx.x & 31, head = blockIdx.y;
   const long long first = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * per;
   if (first >= n_rows) return;
@@ -285,23 +284,46 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const PagedDev d, i
   }
   const float2 sc = s >= 0 ? d.scales[layer * d.layer_scales + (size_t)(s >> 4) * d.Hkv + head] : make_float2(0.f, 0.f);
   if (blockIdx.z == 0) {
+    // a lane writes 16 bytes of a row
+    constexpr int E = OUT == KVS_BF16 ? 8 : 4, LPR = D / E, RPP = 32 / LPR > 0 ? 32 / LPR : 1;
+    const uint8_t* kbase = d.k + layer * d.layer_bytes;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int piece = i * 32 + lane, j = piece / CH, c = piece % CH;
+    for (int r0 = 0; r0 < 16; r0 += RPP) {
+      if (r0 >= n) break;
+      const int j = r0 + lane / LPR, dim = lane % LPR * E;
       const int sj = __shfl_sync(0xffffffffu, s, j & 15);
       const float scale = __shfl_sync(0xffffffffu, sc.x, j & 15);
-      if (piece >= 16 * CH || j >= n) continue;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (sj >= 0)
-        w = __ldg(reinterpret_cast<const uint4*>(d.k + layer * d.layer_bytes + ((size_t)(sj >> 4) * d.Hkv + head) * (16 * D) +
-                                                 k_code(D, sj & 15, c * 16)));
-      const uint32_t* p = &w.x;
-      const size_t e = ((size_t)(i0 + j) * d.Hkv + head) * D + c * 16;
+      if (j >= n || j >= r0 + RPP) continue;
+      uint32_t c[E / 4] = {};
+      if (sj >= 0) {
+        const uint8_t* at = kbase + ((size_t)(sj >> 4) * d.Hkv + head) * (16 * D) + k_code(D, sj & 15, dim);
+        if constexpr (E == 8) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+          c[0] = v.x;
+          c[1] = v.y;
+        } else {
+          c[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+        }
+      }
+      float f[E];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float2 a = e4m3x2_to_float2(p[u] & 0xffffu), b = e4m3x2_to_float2(p[u] >> 16);
-        const float f[4] = {a.x * scale, a.y * scale, b.x * scale, b.y * scale};
-        store4<OUT>(k, e + 4 * u, f);
+      for (int u = 0; u < E / 2; ++u) {
+        const float2 v = e4m3x2_to_float2(c[u / 2] >> (u & 1 ? 16 : 0) & 0xffffu);
+        f[2 * u] = v.x * scale;
+        f[2 * u + 1] = v.y * scale;
+      }
+      const size_t e = ((size_t)(i0 + j) * d.Hkv + head) * D + dim;
+      if constexpr (E == 8) {
+        uint4 o;
+        uint32_t* p = &o.x;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * u], f[2 * u + 1]);
+          p[u] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(k) + e) = o;
+      } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(k) + e) = make_float4(f[0], f[1], f[2], f[3]);
       }
     }
     return;
