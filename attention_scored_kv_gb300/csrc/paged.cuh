@@ -22,6 +22,7 @@ namespace kvs {
 
 constexpr int kScaleMinExp = -100;       // exponents a page scale can have
 constexpr int kScaleMaxExp = 119;
+constexpr float kFloatMax = 3.402823466e38f;
 constexpr int kMaxGroup = 64;            // query heads per KV head at most
 
 struct PagedDev {

@@ -21,6 +21,8 @@ struct kvs_paged {
 
 namespace {
 
+constexpr int32_t kMaxStride = 1 << 22, kMaxReqs = 1 << 20;   // of block tables: positions and tile counts fit 32 bits
+
 void put(char* msg, size_t n, const char* fmt, ...) {
   if (!msg || n == 0) return;
   va_list ap;
@@ -153,9 +155,10 @@ PagedAttendPlan plan_attend(const kvs_paged* pc, int n_reqs, int stride, int tot
 
 kvs_status check_attend(kvs_paged* pc, int32_t n_reqs, int32_t table_stride, int32_t total_q, int32_t max_q_len,
                         bool mass) {
-  if (n_reqs < 1) return fail(pc, KVS_ERR_INVALID_ARGUMENT, "n_reqs must be >= 1 (got %d)", n_reqs);
-  if (table_stride < 1 || table_stride > (1 << 26))
-    return fail(pc, KVS_ERR_INVALID_ARGUMENT, "table_stride must be in [1, 2^26] (got %d)", table_stride);
+  if (n_reqs < 1 || n_reqs > kMaxReqs)
+    return fail(pc, KVS_ERR_INVALID_ARGUMENT, "n_reqs must be in [1, 2^20] (got %d)", n_reqs);
+  if (table_stride < 1 || table_stride > kMaxStride)
+    return fail(pc, KVS_ERR_INVALID_ARGUMENT, "table_stride must be in [1, 2^22] (got %d)", table_stride);
   if (total_q < 0 || max_q_len < 1 || total_q > (1 << 28))
     return fail(pc, KVS_ERR_INVALID_ARGUMENT, "total_q must be in [0, 2^28] and max_q_len >= 1 (got %d, %d)", total_q,
                 max_q_len);
@@ -247,9 +250,9 @@ kvs_status kvs_paged_plan(kvs_paged* pc, int32_t n_reqs, const int32_t* d_ctx_le
                           int32_t* d_row_start, int32_t* d_kv_len, int32_t* d_slots, int32_t* d_positions_opt,
                           int32_t row_capacity, int32_t* d_denied_opt, kvs_stream_t stream) {
   ENTER("kvs_paged_plan");
-  if (n_reqs < 1 || n_reqs > (1 << 24)) return fail(pc, KVS_ERR_INVALID_ARGUMENT, "n_reqs must be in [1, 2^24] (got %d)", n_reqs);
-  if (table_stride < 1 || table_stride > (1 << 26))
-    return fail(pc, KVS_ERR_INVALID_ARGUMENT, "table_stride must be in [1, 2^26] (got %d)", table_stride);
+  if (n_reqs < 1 || n_reqs > kMaxReqs) return fail(pc, KVS_ERR_INVALID_ARGUMENT, "n_reqs must be in [1, 2^20] (got %d)", n_reqs);
+  if (table_stride < 1 || table_stride > kMaxStride)
+    return fail(pc, KVS_ERR_INVALID_ARGUMENT, "table_stride must be in [1, 2^22] (got %d)", table_stride);
   if (free_capacity < 0 || row_capacity < 0 || row_capacity > (1 << 30))
     return fail(pc, KVS_ERR_INVALID_ARGUMENT, "free_capacity and row_capacity must be >= 0, the latter at most 2^30");
   if (!d_ctx_len || !d_new_len || !d_block_table || !d_free_count_in || !d_free_count_out || !d_row_start || !d_kv_len ||
@@ -267,9 +270,9 @@ kvs_status kvs_paged_slot_map(kvs_paged* pc, int32_t n_reqs, const int32_t* d_fi
                               const int32_t* d_block_table, int32_t table_stride, int32_t* d_row_start,
                               int32_t* d_slots, int32_t* d_positions_opt, int32_t row_capacity, kvs_stream_t stream) {
   ENTER("kvs_paged_slot_map");
-  if (n_reqs < 1 || n_reqs > (1 << 24)) return fail(pc, KVS_ERR_INVALID_ARGUMENT, "n_reqs must be in [1, 2^24] (got %d)", n_reqs);
-  if (table_stride < 1 || table_stride > (1 << 26))
-    return fail(pc, KVS_ERR_INVALID_ARGUMENT, "table_stride must be in [1, 2^26] (got %d)", table_stride);
+  if (n_reqs < 1 || n_reqs > kMaxReqs) return fail(pc, KVS_ERR_INVALID_ARGUMENT, "n_reqs must be in [1, 2^20] (got %d)", n_reqs);
+  if (table_stride < 1 || table_stride > kMaxStride)
+    return fail(pc, KVS_ERR_INVALID_ARGUMENT, "table_stride must be in [1, 2^22] (got %d)", table_stride);
   if (row_capacity < 0 || row_capacity > (1 << 30)) return fail(pc, KVS_ERR_INVALID_ARGUMENT, "row_capacity must be in [0, 2^30]");
   if (!d_len || !d_block_table || !d_row_start || (row_capacity && !d_slots) || (row_capacity && d_slots == d_positions_opt))
     return fail(pc, KVS_ERR_INVALID_ARGUMENT, "a required array is NULL, or slots and positions are one array");
@@ -282,9 +285,9 @@ kvs_status kvs_paged_release(kvs_paged* pc, int32_t n_reqs, const int32_t* d_kv_
                              int32_t table_stride, int32_t* d_free_pages, int32_t free_capacity,
                              int32_t* d_free_count, kvs_stream_t stream) {
   ENTER("kvs_paged_release");
-  if (n_reqs < 1 || n_reqs > (1 << 24)) return fail(pc, KVS_ERR_INVALID_ARGUMENT, "n_reqs must be in [1, 2^24] (got %d)", n_reqs);
-  if (table_stride < 1 || table_stride > (1 << 26))
-    return fail(pc, KVS_ERR_INVALID_ARGUMENT, "table_stride must be in [1, 2^26] (got %d)", table_stride);
+  if (n_reqs < 1 || n_reqs > kMaxReqs) return fail(pc, KVS_ERR_INVALID_ARGUMENT, "n_reqs must be in [1, 2^20] (got %d)", n_reqs);
+  if (table_stride < 1 || table_stride > kMaxStride)
+    return fail(pc, KVS_ERR_INVALID_ARGUMENT, "table_stride must be in [1, 2^22] (got %d)", table_stride);
   if (free_capacity < 0) return fail(pc, KVS_ERR_INVALID_ARGUMENT, "free_capacity must be >= 0");
   if (!d_kv_len || !d_block_table || !d_free_count || (free_capacity && !d_free_pages))
     return fail(pc, KVS_ERR_INVALID_ARGUMENT, "a required array is NULL");
@@ -319,7 +322,7 @@ kvs_status kvs_paged_gather(kvs_paged* pc, int32_t layer, int32_t n_rows, const 
 size_t kvs_paged_attend_scratch_bytes(const kvs_paged* pc, int32_t n_reqs, int32_t table_stride, int32_t total_q,
                                       int32_t max_q_len, int32_t block_mass) {
   Trace trace_("kvs_paged_attend_scratch_bytes");
-  if (!pc || n_reqs < 1 || table_stride < 1 || table_stride > (1 << 26) || total_q < 0 || total_q > (1 << 28) ||
+  if (!pc || n_reqs < 1 || n_reqs > kMaxReqs || table_stride < 1 || table_stride > kMaxStride || total_q < 0 || total_q > (1 << 28) ||
       max_q_len < 1 || (block_mass && max_q_len != 1))
     return 0;
   const size_t n = plan_attend(pc, n_reqs, table_stride, total_q, max_q_len, block_mass != 0).total;
@@ -355,7 +358,7 @@ kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const 
   a.table_stride = table_stride;
   a.total_q = total_q;
   a.max_q_len = max_q_len;
-  a.window = window;
+  a.window = window < table_stride * kBlock ? window : 0;     // a longer one hides nothing
   a.table = d_block_table;
   a.kv_len = d_kv_len;
   a.row_start = d_row_start;

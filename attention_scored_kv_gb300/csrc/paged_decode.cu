@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
         *reinterpret_cast<uint32_t*>(base + k_code(D, row, dim)) = hi[0] | hi[1] << 16;
         *reinterpret_cast<uint32_t*>(base + k_code(D, row + RT, dim)) = lo[0] | lo[1] << 16;
       }
-      if (part == 0) ms.qc[buf][row] = live ? exp2_int(e) * qk : 0.f;
+      if (part == 0) ms.qc[buf][row] = !live ? 0.f : amax <= kFloatMax ? exp2_int(e) * qk : NAN;
       umma::fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready));
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
             grew = true;
           }
           m[r] = now;
-          x[r] = now > -INFINITY ? ex2(x[r] - now) : 0.f;
+          x[r] = ex2(x[r] - (now > -INFINITY ? now : 0.f));       // hidden: 2^-inf; a NaN stays one
           l[r] = fmaf(l[r], f[r], x[r] * iv);
         }
         if (MASS) {
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
         for (int r = 0; r < RT; ++r) {
           if (r < rows && tid < D)
             out[((size_t)(w.u.first + r / d.G) * d.Hq + w.h * d.G + r % d.G) * D + tid] =
-                __float2bfloat16_rn(l[r] > 0.f ? o[r] / l[r] : 0.f);
+                __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
           if (MASS && r < rows && tid == r) a.lse[(size_t)w.r * d.Hq + w.h * d.G + r] = m[r] + log2f(l[r]);
         }
       } else {
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttend a,
 #pragma unroll
     for (int k = 1; k < kJoinThreads / D; ++k) acc += acc_of[tid + k * D];
     static_cast<__nv_bfloat16*>(a.out)[((size_t)(u.first + row / d.G) * d.Hq + hq) * D + tid] =
-        __float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f);
+        __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
   }
   if (MASS && tid == 0) a.lse[(size_t)r * d.Hq + hq] = top + log2f(sum);
 }

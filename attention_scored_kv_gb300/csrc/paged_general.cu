@@ -46,11 +46,26 @@ __device__ __forceinline__ RowRange row_range(const PagedAttend& a, int t) {
     x.r = request_of(a.row_start, a.n_reqs, t);
     first = __ldg(a.row_start + x.r);
     n = __ldg(a.row_start + x.r + 1) - first;
-    if (t - first >= a.max_q_len) { x.live = false; return x; }
+    if (t < first || t - first >= a.max_q_len) { x.live = false; return x; }
   }
   const int len = min(max(__ldg(a.kv_len + x.r), 0), a.table_stride * kBlock);
   const int p = len - n + (t - first);           // the row's position
-  x.hi = max(p + 1, 0);
+  x.hi = min(max(p + 1, 0), len);
+  x.lo = a.window > 0 ? max(0, x.hi - a.window) : 0;
+  return x;
+}
+
+// What the one row of request r sees, in a call of single-token rows.
+__device__ __forceinline__ RowRange request_range(const PagedAttend& a, int r) {
+  RowRange x{r, true, 0, 0};
+  int n = 1;
+  if (a.row_start) {
+    const int first = __ldg(a.row_start + r);
+    n = __ldg(a.row_start + r + 1) - first;
+    x.live = n > 0 && first >= 0 && first < a.total_q;
+  }
+  const int len = min(max(__ldg(a.kv_len + r), 0), a.table_stride * kBlock);
+  x.hi = min(max(len - n + 1, 0), len);
   x.lo = a.window > 0 ? max(0, x.hi - a.window) : 0;
   return x;
 }
@@ -187,7 +202,7 @@ __global__ void __launch_bounds__(kWarps * 32) general_kernel(const PagedAttend 
       }
       const int hq = head * d.G + g0 + g;
       if (a.splits == 1) {
-        store1<DT>(a.out, ((size_t)t * d.Hq + hq) * D + dim, sum > 0.f ? acc / sum : 0.f);
+        store1<DT>(a.out, ((size_t)t * d.Hq + hq) * D + dim, sum == 0.f ? 0.f : acc / sum);
         if (a.lse && dim == 0) a.lse[(size_t)x.r * d.Hq + hq] = top + log2f(sum);
       } else {
         const size_t rec = ((size_t)t * d.Hq + hq) * a.splits + part;
@@ -216,7 +231,7 @@ __global__ void __launch_bounds__(kWarps * 32) general_join_kernel(const PagedAt
   for (int dim = lane; dim < D; dim += 32) {
     float acc = 0.f;
     for (int k = 0; k < a.splits; ++k) acc += a.part_o[(rec + k) * D + dim] * exp2f(a.part_ml[rec + k].x - ref);
-    store1<DT>(a.out, (size_t)u * D + dim, sum > 0.f ? acc / sum : 0.f);
+    store1<DT>(a.out, (size_t)u * D + dim, sum == 0.f ? 0.f : acc / sum);
   }
   if (a.lse && lane == 0) a.lse[(size_t)x.r * d.Hq + hq] = top + log2f(sum);
 }
@@ -226,7 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32) general_join_kernel(const PagedAt
 constexpr int kMassBlocks = 16;          // of a warp
 __global__ void __launch_bounds__(kWarps * 32) mass_kernel(const PagedAttend a) {
   const int lane = threadIdx.x & 31, r = blockIdx.x, Hq = a.d.Hq;
-  const RowRange x = row_range(a, r);
+  const RowRange x = request_range(a, r);
   const int b1 = x.live && x.hi > x.lo ? (x.hi + kBlock - 1) / kBlock : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int first = x.lo / kBlock + (blockIdx.y * kWarps + (threadIdx.x >> 5)) * kMassBlocks;

@@ -370,10 +370,11 @@ __global__ void __launch_bounds__(kRows) split_kernel(const PagedAttend a, const
   for (int j = 0; j < D / 8; ++j)
 #pragma unroll
     for (int u = 0; u < 4; ++u) top2 = __hmax2(top2, __habs2(reinterpret_cast<const __nv_bfloat162*>(&raw[j])[u]));
-  const int e = scale_exp(fmaxf(__low2float(top2), __high2float(top2)));
+  const float amax = fmaxf(__low2float(top2), __high2float(top2));
+  const int e = scale_exp(amax);
   const uint64_t up = pack2(exp2_int(-e), exp2_int(-e));
   const size_t at = (size_t)id * d.Hkv + h;
-  a.q_factors[at * kRows + row] = exp2_int(live ? e : 0) * (kLog2e * rsqrtf((float)D));
+  a.q_factors[at * kRows + row] = amax <= kFloatMax ? exp2_int(live ? e : 0) * (kLog2e * rsqrtf((float)D)) : NAN;
   uint8_t* out = a.q_pieces + at * (kRows * 2 * D) + row * 16;
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       umma::fence_after();
       const bool live = token < qpt && i < w.u.cnt;
       if (w.whole) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
             (live ? ((size_t)(w.q.first + w.u.i0 + i) * d.Hq + w.h * d.G + head) * D : 0);
 #pragma unroll
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAt
       acc[q4].w = fmaf(v.w, f, acc[q4].w);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                        ((size_t)(q.first + u.i0 + i) * d.Hq + h * d.G + row % d.G) * D;
 #pragma unroll

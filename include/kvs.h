@@ -490,8 +490,9 @@ KVS_API uint32_t kvs_build_info(void);
  * the smallest normal code.
  *
  * Tables and lengths are the caller's device arrays.  A request r is row r of them:
- *   block_table  [n_reqs][table_stride] int32, entry b the page of positions
- *                16 b .. 16 b + 15; entries past a request's length are not read
+ *   block_table  [n_reqs][table_stride] int32 (n_reqs <= 2^20, table_stride <= 2^22), entry b
+ *                the page of positions 16 b .. 16 b + 15; entries past a request's length
+ *                are not read
  *   slot         page * 16 + position % 16; negative = none
  *   rows         new tokens are packed by request: rows row_start[r] .. row_start[r+1]-1
  * A page in a table or slot that is not in [0, num_pages) is never followed: the token or
@@ -607,7 +608,8 @@ KVS_API kvs_status kvs_paged_gather(kvs_paged* pc, int32_t layer, int32_t n_rows
  * row_start[r+1]-1 are the last tokens of request r, oldest first: the i-th of n is at
  * position kv_len[r] - n + i and sees the positions up to its own, with window > 0 only the
  * last `window` of them.  Logits q.k/sqrt(D); softmax per head; query head h reads KV head
- * h / (Hq / Hkv).  A row that sees nothing gets zeros.  Rows past row_start[n_reqs] are left
+ * h / (Hq / Hkv).  A row that sees nothing gets zeros; one whose query is not finite
+ * gets NaN.  Rows past row_start[n_reqs] are left
  * as they were.  d_row_start NULL: one row per request (total_q must be n_reqs).
  * max_q_len: at least the most rows any request has (1 when d_row_start is NULL); rows past
  * it, or past total_q, are left as they were and reported as KVS_ERR_CAPACITY.  kv_len is

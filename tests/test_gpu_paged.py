@@ -388,6 +388,72 @@ def test_lengths_past_what_the_host_said(dt):
     assert (out[4:6] == 9.0).all()
 
 
+@pytest.mark.parametrize("dt", [kvs.BF16, kvs.F32])
+@pytest.mark.parametrize("n,new", [(700, 1), (600, 5), (1100, 1)])
+def test_many_requests(dt, n, new):
+    """More requests than the kernels look at in one round, some without rows."""
+    rng = np.random.default_rng(n)
+    news = rng.integers(0, new + 1, n)
+    kv = np.maximum(rng.integers(0, 40, n), news)
+    cache, orc, table, q = filled(kv, news, 8, 1, 64, dt, seed=n)
+    start = np.concatenate([[0], np.cumsum(news)])
+    want = orc.attend(f64(q), table, kv, start)
+    out = cache.attend(0, q.cuda(), i32(table), i32(kv), q_start=i32(start), max_q_len=new)
+    check_out(out, want, 64, dt, dt == kvs.BF16)
+    if new == 1:
+        mass = torch.full(table.shape, -3.0, device="cuda")
+        out = cache.attend(0, q.cuda(), i32(table), i32(kv), q_start=i32(start), block_mass=mass)
+        check_out(out, want, 64, dt, dt == kvs.BF16)
+        check_mass(mass, want, np.arange(table.shape[1])[None] >= -(-(kv * news)[:, None] // 16), 64)
+    assert cache.get_status() == 0
+
+
+@pytest.mark.parametrize("dt", [kvs.BF16, kvs.F32])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_queries_that_are_not_finite(dt, new):
+    """A query with a NaN or an infinity spoils its own row and head, no other."""
+    kv = [90, 200]
+    cache, orc, table, q = filled(kv, [new, new], 16, 2, 128, dt, seed=12)
+    start = [0, new, 2 * new]
+    want = orc.attend(f64(q), table, kv, start)
+    bad = q.clone()
+    bad[0, 3, 5], bad[new, 9, 127], bad[2 * new - 1, 15, 0] = float("nan"), float("inf"), float("-inf")
+    out = cache.attend(0, bad.cuda(), i32(table), i32(kv), q_start=i32(start), max_q_len=new)
+    spoilt = torch.zeros((2 * new, 16), dtype=torch.bool)
+    spoilt[0, 3] = spoilt[new, 9] = spoilt[2 * new - 1, 15] = True
+    assert out.isnan().any(-1).cpu().equal(spoilt)
+    keep = (~spoilt).numpy()
+    out[spoilt.cuda()] = 0
+    zero = {k: np.where(keep.reshape(keep.shape + (1,) * (v.ndim - 2)), v, 0.0) for k, v in want.items() if k != "mass"}
+    check_out(out, zero, 128, dt, dt == kvs.BF16)
+    assert cache.get_status() == 0
+
+
+@pytest.mark.parametrize("dt", [kvs.BF16, kvs.F32])
+def test_row_starts_that_are_not_sorted(dt):
+    """Row starts out of range or falling are reported; rows of the requests that are in order are right."""
+    kv, new = [50, 60, 70], [2, 2, 2]
+    cache, orc, table, q = filled(kv, new, 16, 2, 128, dt, seed=13)
+    want = orc.attend(f64(q), table, kv, [0, 2, 4, 6])
+    for start, good in (([0, 2, 1, 1], [0, 1]), ([-3, 2, 4, 6], [2, 3, 4, 5]), ([0, 2, 4, 9], [0, 1, 2, 3])):
+        for most in (2, 9):
+            out = cache.attend(0, q.cuda(), i32(table), i32(kv), q_start=i32(start), max_q_len=most)
+            if dt == kvs.BF16:              # the other path looks rows up by their starts, which need an order
+                check_out(out[good], {k: v[good] for k, v in want.items() if k != "mass"}, 128, dt, True)
+            assert cache.get_status() == _abi.ERR_CAPACITY
+            cache.clear_error()
+
+
+def test_windows_past_every_length():
+    kv, new = [300, 20], [1, 1]
+    cache, orc, table, q = filled(kv, new, 8, 1, 64, kvs.BF16, seed=14)
+    plain = cache.attend(0, q.cuda(), i32(table), i32(kv))
+    for window in (300, 10 ** 6, 2 ** 31 - 1):
+        assert torch.equal(cache.attend(0, q.cuda(), i32(table), i32(kv), window=window), plain)
+    rag = cache.attend(0, q.cuda(), i32(table), i32(kv), q_start=i32([0, 1, 2]), max_q_len=50)
+    assert torch.equal(cache.attend(0, q.cuda(), i32(table), i32(kv), q_start=i32([0, 1, 2]), max_q_len=50, window=2 ** 31 - 1), rag)
+
+
 # ------------------------------------------------------------------ a run of them together
 def step_graph(cache, st, layers, cap, q_len):
     """One step as a program would capture it: everything from static tensors."""
@@ -535,6 +601,8 @@ def test_refusals():
     cache.append(0, one[:0], one[:0], s3[:0])
     assert cache.gather(0, s3[:0])[0].shape == (0, 2, 32)
     assert cache.attend(0, qd[:0], t, ln, q_start=i32([0, 0, 0])).shape == (0, 4, 32)
+    wide = torch.zeros((1, (1 << 22) + 1), dtype=torch.int32, device="cuda")
+    refused(inv, cache.attend, 0, qd[:1], wide, ln[:1], scratch=torch.zeros(1 << 20, dtype=torch.uint8, device="cuda"))
     with pytest.raises(kvs.KVSError):
         make(d=96)
     with pytest.raises(kvs.KVSError):
