@@ -3,15 +3,19 @@
 Each CUDA translation unit is compiled in parallel to an object under _build/, then
 linked into attention_scored_kv_gb300/_lib/libkvs.so.  The same sources built with
 -DKVS_DEBUG (device-side bounds checks, NaN-poisoned scratch) give _lib/libkvs_debug.so,
-which the binding loads when KVS_LIB_VARIANT=debug.  No cmake, no torch extension
+which the binding loads when KVS_LIB_VARIANT=debug.  One host file, csrc/paged_call.cpp,
+becomes the Python extension _lib/_paged_call.so with g++ against torch's headers: the
+binding's own checks and allocations, without kernels.  No cmake, no torch extension
 machinery: plain nvcc, one -gencode.  Rebuilds only what changed (by mtime).
 """
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +24,8 @@ BUILD = os.path.join(HERE, "_build")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libkvs.so")
 LIB_DEBUG = os.path.join(LIBDIR, "libkvs_debug.so")
+CALL_SRC = os.path.join(CSRC, "paged_call.cpp")
+CALL = os.path.join(LIBDIR, "_paged_call.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -63,6 +69,25 @@ def _link(objs, lib):
             raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
 
 
+def _build_call():
+    """The binding's extension module."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    newest = max(os.path.getmtime(CALL_SRC), os.path.getmtime(os.path.join(INCLUDE, "kvs.h")))
+    if os.path.exists(CALL) and os.path.getmtime(CALL) >= newest:
+        return
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    dirs = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden"]
+    for d in dirs:
+        cmd += ["-isystem", d]
+    cmd += [CALL_SRC, "-o", CALL, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch",
+            "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (CALL_SRC, " ".join(cmd), r.stderr))
+
+
 def build(verbose=False, ptxas_info=False, debug=True):
     """Compile every translation unit and link libkvs.so (and, with debug, the checked
     variant libkvs_debug.so); returns the release library's path."""
@@ -75,8 +100,10 @@ def build(verbose=False, ptxas_info=False, debug=True):
     jobs = [(src, extra, BUILD) for src in srcs]
     if debug:
         jobs += [(src, ["-DKVS_DEBUG"], dbg_dir) for src in srcs]
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(jobs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(jobs) + 1)) as ex:
+        call = ex.submit(_build_call)
         results = list(ex.map(lambda j: _compile(*j), jobs))
+        call.result()
     if verbose:
         for _, log in results:
             if log:

@@ -13,7 +13,8 @@
 // Precision: E4M3 holds 4 significant bits.  A bf16 query (8 bits) is split in two pieces
 // of 4, hi = rn(q), lo = rn(16 (q - hi)) after a power of two brings the row's largest to
 // (224, 448]: exact for elements within 2^14 of it.  A probability is split the same way:
-// its 8 bits cost 2^-8 relative, half of what rounding the output to bf16 may.  The pieces are
+// its 8 bits are off by at most 2^-9 of it, half of what rounding the output to bf16 may
+// be.  The pieces are
 // separate columns of the same instruction, N = 2 rows, so 8 rows fill its smallest N of
 // 16 and the split is free there.  Accumulation is float32.
 //

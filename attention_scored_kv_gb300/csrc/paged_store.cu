@@ -15,7 +15,6 @@
 // then are values looked at one by one.  The row that starts a run leads it; others exit, so
 // a batch of single tokens is one warp per token and cache, and rows of a long prompt are
 // taken sixteen to a warp to spare idle warps.
-#include "append_store.cuh"
 #include "paged.cuh"
 
 namespace kvs {

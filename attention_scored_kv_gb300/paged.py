@@ -7,6 +7,9 @@ graph and replayed while the batch changes.
 
 import collections
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
@@ -43,11 +46,36 @@ def paged_workspace_bytes(cfg):
     return int(lib().kvs_paged_workspace_bytes(ctypes.byref(cfg)))
 
 
+_call = None
+
+
+def _load_call():
+    """The extension that makes the calls of a decode step (csrc/paged_call.cpp), bound to the loaded library."""
+    global _call
+    if _call is None:
+        path = os.path.join(os.path.dirname(_abi.LIB_PATH), "_paged_call.so")
+        if not os.path.exists(path):
+            raise RuntimeError("_paged_call.so is not built (%s); run python -m attention_scored_kv_gb300.build" % path)
+        loader = importlib.machinery.ExtensionFileLoader("_paged_call", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_paged_call", loader))
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib(), "kvs_paged_" + f), ctypes.c_void_p).value
+                      for f in ("plan", "append", "gather", "attend", "attend_scratch_bytes")))
+        _call = module
+    return _call
+
+
 class PagedCache:
     """A kvs_paged context bound to a workspace this object owns (a torch uint8 tensor).
 
     Work goes on `stream`, by default the current stream of the cache's device.  Outputs
-    that a method allocates are safe to use on that stream."""
+    that a method allocates are safe to use on that stream.
+
+    plan, append, gather and attend on the current stream, with outputs of their own, are
+    taken by an extension module; it declines what it does not find in order, and the
+    method's own checks say why."""
+
+    _fast = None
 
     def __init__(self, cfg, device=None, stream=None):
         st, msg = validate_paged_config(cfg)
@@ -69,6 +97,8 @@ class PagedCache:
         self.in_dtype = _TORCH_DT[cfg.in_dtype]
         self._row = (int(cfg.num_kv_heads), int(cfg.head_dim))
         self._qrow = (int(cfg.num_q_heads), int(cfg.head_dim))
+        self._fast = _load_call()
+        self._key = (self._ctx.value, self._index, self._row[0], self._qrow[0], self._row[1], cfg.in_dtype == _abi.BF16)
 
     def __del__(self):
         if getattr(self, "_ctx", None) and self._ctx.value:
@@ -116,6 +146,13 @@ class PagedCache:
         Fills block_table [n, stride] in place; pages come from the stack free_pages
         [capacity] whose size is free_count [1].  free_count_out (default: free_count)
         and kv_len_out (may be ctx_len) receive the updated state.  Returns a PagedPlan."""
+        if stream is None and kv_len_out is None and self._fast is not None:
+            r = self._fast.plan(self._key, ctx_len, new_len, block_table, free_pages, free_count,
+                                free_count if free_count_out is None else free_count_out, row_capacity)
+            if r.__class__ is tuple:
+                return PagedPlan(*r)
+            if r is not None:
+                self._check(r)
         n, = self._need_dims(ctx_len, "ctx_len", _i32, 1)
         stride = self._need_dims(block_table, "block_table", _i32, 2)[1]
         cap, = self._need_dims(free_pages, "free_pages", _i32, 1)
@@ -172,6 +209,12 @@ class PagedCache:
     # ---- tokens
     def append(self, layer, k, v, slots, stream=None):
         """Store k, v [rows, Hkv, D] (input dtype) at slots [rows]."""
+        if stream is None and self._fast is not None:
+            st = self._fast.append(self._key, layer, k, v, slots)
+            if st == 0:
+                return
+            if st is not None:
+                self._check(st)
         n, = self._need_dims(slots, "slots", _i32, 1)
         shape = (n,) + self._row
         st = self._lib.kvs_paged_append(
@@ -182,6 +225,12 @@ class PagedCache:
 
     def gather(self, layer, slots, k_out=None, v_out=None, stream=None):
         """The values at slots [rows]: (k, v), each [rows, Hkv, D] in the input dtype."""
+        if stream is None and k_out is None and v_out is None and self._fast is not None:
+            r = self._fast.gather(self._key, layer, slots)
+            if r.__class__ is tuple:
+                return r
+            if r is not None:
+                self._check(r)
         n, = self._need_dims(slots, "slots", _i32, 1)
         shape = (n,) + self._row
         if k_out is None:
@@ -207,6 +256,12 @@ class PagedCache:
         tokens, at most max_q_len of them.  window > 0: only the last `window` positions.
         block_mass: optional float32 [n, stride] that receives each visible block's mass
         (single-token rows only).  scratch: optional uint8 tensor of attend_scratch_bytes."""
+        if stream is None and out is None and scratch is None and self._fast is not None:
+            r = self._fast.attend(self._key, layer, q, block_table, kv_len, q_start, max_q_len, window, block_mass)
+            if r.__class__ is _Tensor:
+                return r
+            if r is not None:
+                self._check(r)
         n, = self._need_dims(kv_len, "kv_len", _i32, 1)
         stride = self._need_dims(block_table, "block_table", _i32, 2)[1]
         rows = self._need_dims(q, "q", self.in_dtype, 3)[0]

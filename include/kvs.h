@@ -620,8 +620,8 @@ KVS_API kvs_status kvs_paged_gather(kvs_paged* pc, int32_t layer, int32_t n_rows
  * that the row sees a part of; other entries are left as they were.
  * d_scratch: device memory of kvs_paged_attend_scratch_bytes(), 256-byte aligned, whose
  * contents before and after mean nothing; calls that may overlap need scratch of their
- * own.  Probabilities are rounded to 16 bits or finer before their product with V (bf16
- * in_dtype); sums and softmax statistics are float32. */
+ * own.  With bf16 in_dtype probabilities are rounded to 8 significant bits or more before
+ * their product with V; sums and softmax statistics are float32. */
 KVS_API size_t kvs_paged_attend_scratch_bytes(const kvs_paged* pc, int32_t n_reqs, int32_t table_stride,
                                               int32_t total_q, int32_t max_q_len, int32_t block_mass);
 KVS_API kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const int32_t* d_block_table,

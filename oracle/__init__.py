@@ -26,11 +26,14 @@ What it computes, each piece citing the page passage it follows:
                    protected regions.
 * ``snapkv``     - SnapKV prefill scoring: observation-window votes, max-pooled with
                    kernel 7 ("Context views at marginal cost", per-system reductions).
+* ``paged``      - the paged cache: block tables and slots from request lengths, E4M3
+                   pages with a power-of-two scale per page and KV head, attention of
+                   packed ragged queries, block masses.
 * ``memory``     - the KV memory arithmetic ("Context Optimization", Memory Budget
                    Calculator).
 
 Parity status per function is listed in each module header.
 """
 
-from . import e4m3, attention, selection, memory, slot_cache, snapkv, cache  # noqa: F401
+from . import e4m3, attention, selection, memory, slot_cache, snapkv, cache, paged  # noqa: F401
 from .cache import OracleKV  # noqa: F401

@@ -13,12 +13,13 @@ element, with A = sum_j a_j |v_j| from the oracle and u = eps/2 of the output ty
   and exp2 and the subtraction of the maximum add 2^-21 (1 + |s|), |s| <= that sum.  A
   normalised probability is off by twice that relatively (itself and the sum), four times
   with the statistics' own rounding.
-  r: what a probability is rounded to before its product with V: 2^-8 where it is kept in
+  r: what a probability is rounded to before its product with V: 2^-9 where it is kept in
   two 8-bit pieces of 4 significant bits each, 2^-11 in f16, covered by 2^-8 for both; the
   float32 path keeps 2^-23 (D of its roundings are in delta's term).
   F: rounding is relative only down to the smallest step.  The tensor-core decode keeps x =
   a_j * (V scale), relative to its largest, as 2^8 at most; E4M3's smallest step is 2^-9 and
-  the second piece carries a factor of 32, so x is off by up to 2^-15, 2^-23 of the largest,
+  the second piece carries a factor of 32, so x is off by up to 2^-15, 2^-23 of the largest
+  (the prompt kernel keeps x as 1 or more at its largest, in f16, whose smallest half step is 2^-25),
   against each code: F = max_j(a_j * V scale) sum_j |V code|.  (A page's scale is at least its
   largest value / 448, so F matters only where the heaviest tokens' own values vanish.)
 """
@@ -553,6 +554,42 @@ def test_two_streams_at_once():
     for x, y in got:
         assert torch.equal(x, want) and torch.equal(y, want2)
     check_out(want, orc.attend(f64(q), table, kv), 128, kvs.BF16, True)
+
+
+@pytest.mark.parametrize("dt", [kvs.BF16, kvs.F32])
+def test_both_ways_of_calling(dt):
+    """The extension and the methods' own path give the same bytes and refuse the same calls."""
+    kv, new = [100, 37, 250], [1, 1, 1]
+    cache, _, table, q = filled(kv, new, 8, 2, 64, dt, seed=20)
+    t, ln, qd = i32(table), i32(kv), q.cuda()
+    g = torch.Generator().manual_seed(1)
+    k, v = rand(g, (20, 2, 64), dt).cuda(), rand(g, (20, 2, 64), dt).cuda()
+    slots = i32(16 * int(table[0, 0]) + np.arange(20) % 16)[:16]
+    k, v = k[:16], v[:16]
+    results = []
+    for fast in (cache._fast, None):
+        cache._fast = fast
+        free, count, tab = i32(np.arange(30)), i32([30]), torch.full((3, 20), -1, dtype=torch.int32, device="cuda")
+        p = cache.plan(i32([0, 5, 16]), i32([17, 3, 0]), tab, free, count, 23)
+        cache.append(0, k, v, slots)
+        mass = torch.zeros(t.shape, device="cuda")
+        results.append([tab, count, *p, *cache.gather(0, slots), cache.attend(0, qd, t, ln, block_mass=mass), mass,
+                        cache.attend(0, qd, t, ln, q_start=i32([0, 1, 2, 3]), max_q_len=50, window=33)])
+        for call in (lambda: cache.append(0, k, v, slots.long()), lambda: cache.gather(0, slots.cpu()),
+                     lambda: cache.attend(0, qd.double(), t, ln), lambda: cache.plan(ln, ln, t.float(), ln, count, 3)):
+            with pytest.raises(TypeError):
+                call()
+        for call in (lambda: cache.append(3, k, v, slots), lambda: cache.gather(-1, slots), lambda: cache.attend(1, qd, t, ln),
+                     lambda: cache.attend(0, qd, t, ln, max_q_len=2), lambda: cache.plan(ln, ln, t, ln, count, (1 << 30) + 4)):
+            with pytest.raises((kvs.KVSError, torch.OutOfMemoryError)):
+                call()
+        cache.clear_error()
+    for a, b in zip(*results):
+        assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
+    class Own(torch.Tensor):
+        pass
+    out = cache.attend(0, qd.as_subclass(Own), t, ln)
+    assert torch.equal(out, results[0][-3])
 
 
 # ------------------------------------------------------------------ refusals (all on the host, before any launch)
