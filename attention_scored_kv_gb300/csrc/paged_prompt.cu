@@ -5,25 +5,34 @@
 // tiles A and B of 128), which share every K and V they read.  Per 128 cached tokens:
 //   S = Q K^T        two pieces of Q (4 significant bits each) as one contraction of 2 D,
 //                    E4M3 x E4M3, K as it is stored
-//   t = S kscale c_r + log2 vscale,  m_r: a maximum that moves only by steps of 2^8 or more
-//   x = 2^(t - m_r + 6),  l_r += x / vscale,  O += X V      f16 x f16
+//   t = S kscale c_r + log2 vscale,  m_r: a reference at or below the row's maximum so far
+//   x = 2^(t - m_r),  l_r += x / vscale,  O += X V      f16 x f16
 // and o = O / l.  The scales are powers of two, so V's rides in x's exponent and V's codes
-// are exact in f16; x <= 2^14 fits f16, whose 11 bits are finer than the output's 8.
-// Queries: exact down to 2^-10 of the row's largest element, an error of 2^-19 of the
-// largest below that.
+// are exact in f16.  m moves only when a row passes it by 2^15 (x still fits f16, whose 11 bits
+// are finer than the output's 8), which is seen from the sums that l needs anyway; O is
+// then rescaled.  Queries: exact down to 2^-10 of the row's largest element, an error of
+// 2^-19 of the largest below that.
 //
 // How: work is cut as in the decode kernel: the 128-token tiles of all units laid end to
 // end and split evenly over one CTA per SM, partials of split units added by a join
 // kernel.  That also balances causal rows, whose units differ in length, and feeds all
-// SMs when rows are few and the context is long.
-// Per CTA: one warp copies K pages into a ring, four warps convert V's codes to f16 operand
-// rows (a page's rows are its operand rows, so it is load, convert, store), one thread
+// SMs when rows are few and the context is long.  A unit's start counts as two tiles.
+// A split kernel first writes the queries' pieces in operand layout (a few percent of the
+// time; two warps of each CTA that did it took 15 to 27 thousand clocks a unit).
+// Per CTA: one warp copies K pages into a ring, one the queries, four convert V's codes to
+// f16 operand rows (a page's rows are its operand rows, so it is load, convert, store), one
 // issues the matrix instructions, and two groups of four warps do the softmax of A and B, a
-// thread to a row, so that no row statistic crosses threads.  The matrix thread works on
+// thread to a row, so that no row statistic crosses threads.  The matrix warp works on
 // one tile while the other's softmax runs: O(A) += X(A, j) V and S(A, j+1) while B's
 // exponentials are computed, then the reverse.  X goes to TMEM, over S, as the product's
 // first operand: from shared memory the two operands of both products, X's stores and V's
 // would be 368 KB a step, 2900 clocks at 128 bytes, against the tensor core's 2048.
+//
+// Bound by the chain of one tile: softmax (1300 to 1500 clocks), X's store (200), its two
+// products (1300), of which only the other tile's overlap: about 4000 clocks a step of 128
+// tokens, against 2048 of matrix work.  Measured on 32/4 heads of 128: an 8192-token
+// prompt 525 us (1.05 PFLOP/s, 55 % of the measured bf16 rate), five chunks of 100 to 2048
+// tokens behind up to 8192 397 us (945 TFLOP/s).
 #include "paged_mma.cuh"
 
 namespace kvs {
@@ -42,9 +51,8 @@ constexpr int kSetup = 2;                // what a unit's start costs, in tiles,
 constexpr int kRows = 128;               // rows of a tile of queries
 constexpr int kChunk = 512;              // requests of one round of the search
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTop = 0.f;              // x of the maximum when it was taken: 1
 constexpr float kSlack = 15.f;           // the maximum moves when a row passes it by this: x <= 2^15 fits f16
-constexpr float kLimit = 32768.f;        // 2^(kTop + kSlack): more in a block's sum, and the maximum is looked at
+constexpr float kLimit = 32768.f;        // 2^kSlack: more in a block's sum, and the maximum is looked at
 
 // Units of request r: groups of `per` query tokens, all KV heads alike.
 struct Req {
@@ -719,8 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
         uint32_t h[64];
         float f = 1.f, add, big;
         // Within a segment the last maximum mostly serves, so the exponentials are taken at once.  Where a
-        // block's sum passes what the slack allows, the row's maximum moves up by log2 of it (at most 4 too
-        // far) and they are taken again; only where even that overflowed are the maxima looked at.
+        // block's sum passes what the slack allows, the reference moves up by log2 of it, less the 4 that 16
+        // equal terms add, and they are taken again; only where even that overflowed are the maxima looked at.
         bool look = t == 0 || __any_sync(0xffffffffu, m == -INFINITY), last = look;
         for (;;) {
           if (look) {
@@ -730,13 +738,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
               m = top;
             }
           }
-          const float ref = (m == -INFINITY ? 0.f : m) - kTop;
+          const float ref = m == -INFINITY ? 0.f : m;
           add = masked ? row_exp<true>(t_s, y, c, ref, h, big) : row_exp<false>(t_s, y, c, ref, h, big);
           if (last || !__any_sync(0xffffffffu, !(big <= kLimit))) break;
           last = true;
           look = __any_sync(0xffffffffu, !(big < 1e38f));
           if (!look && big > kLimit) {
-            const float up = __log2f(big);
+            const float up = __log2f(big) - 4.f;
             f = ex2(-up);
             m += up;
           }
