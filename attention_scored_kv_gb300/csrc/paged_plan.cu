@@ -271,10 +271,10 @@ cudaError_t launch(const Args& a, int grid, bool cluster, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, plan_kernel<TAKE>, a);
 }
 
-// CTAs that `capacity` rows feed: two rounds of four rows a thread each.
+// CTAs that `capacity` rows feed: two rounds of four rows a thread each, at most four CTAs to an SM.
 int grid_for(int capacity, int sms) {
   const int want = (int)cdiv64(capacity, 2 * 4 * kThreads);
-  return want < 1 ? 1 : (want < sms ? want : sms);
+  return want < 1 ? 1 : (want < 4 * sms ? want : 4 * sms);
 }
 
 }  // namespace
