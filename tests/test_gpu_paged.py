@@ -592,6 +592,54 @@ def test_both_ways_of_calling(dt):
     assert torch.equal(out, results[0][-3])
 
 
+def test_two_graphs_at_once():
+    """Two captured graphs over one cache, replayed on two streams: each has scratch of its own."""
+    kv, new = [1500, 700, 300], [1, 1, 60]
+    cache, orc, table, q = filled(kv, new, 16, 2, 128, kvs.BF16, seed=21)
+    t, ln, qd, st = i32(table), i32(kv), q.cuda(), i32([0, 1, 2, 62])
+    calls = [lambda: cache.attend(0, qd, t, ln, q_start=st, max_q_len=60),
+             lambda: cache.attend(0, qd[:3], t, ln, window=900),
+             lambda: cache.attend(0, qd, t, ln, q_start=st, max_q_len=60, window=50)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append([c() for _ in range(6)])
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for w, many in zip(want, outs):
+        for o in many:
+            assert torch.equal(o, w)
+    assert cache.get_status() == 0
+
+
+@pytest.mark.parametrize("dt", [kvs.BF16, kvs.F32])
+def test_pages_beyond_32_bits(dt):
+    """A pool whose codes pass 4 GB in each of K and V, used at its ends."""
+    pages, hkv, d = 600_000, 4, 128
+    cache, orc = make(16, hkv, d, pages, dt), ref.Pages(40, hkv, d)
+    ids = np.concatenate([np.arange(20), pages - 20 + np.arange(20)])[np.random.default_rng(0).permutation(40)]
+    table, small = ids.reshape(2, 20), np.arange(40).reshape(2, 20)
+    kv, g = [317, 290], torch.Generator().manual_seed(3)
+    slots, own = (np.concatenate([t[r, np.arange(n) // 16] * 16 + np.arange(n) % 16 for r, n in enumerate(kv)]) for t in (table, small))
+    k, v, q = rand(g, (sum(kv), hkv, d), dt), rand(g, (sum(kv), hkv, d), dt), rand(g, (92, 16, d), dt)
+    cache.append(0, k.cuda(), v.cuda(), i32(slots))
+    orc.append(f64(k), f64(v), own)
+    for x, y in zip(cache.gather(0, i32(slots)), orc.gather(own)):
+        assert np.array_equal(f64(x), y)
+    for n in ([1, 1], [2, 90]):
+        start = [0, n[0], n[0] + n[1]]
+        out = cache.attend(0, q[:sum(n)].cuda(), i32(table), i32(kv), q_start=i32(start), max_q_len=max(n))
+        check_out(out, orc.attend(f64(q[:sum(n)]), small, kv, start), d, dt, dt == kvs.BF16)
+    assert cache.get_status() == 0
+
+
 # ------------------------------------------------------------------ refusals (all on the host, before any launch)
 def test_refusals():
     cache, orc, table, q = filled([40, 20], [1, 1], 4, 2, 32, kvs.BF16)
