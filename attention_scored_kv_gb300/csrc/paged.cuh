@@ -47,7 +47,7 @@ struct PagedAttend {
   int32_t splits;          // general kernel: parts of a row's range
   uint8_t* q_pieces;       // prompt kernel: split queries, and their rows' factors
   float* q_factors;
-  int32_t* cuts;           // prompt kernel: 8 words a CTA
+  int32_t* cuts;           // decode and prompt kernels: 8 words a CTA
 };
 
 // How a call runs: a pure function of host-known sizes, so that the scratch size and the

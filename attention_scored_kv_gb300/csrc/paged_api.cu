@@ -152,7 +152,7 @@ PagedAttendPlan plan_attend(const kvs_paged* pc, int n_reqs, int stride, int tot
   const size_t tiles = p.kernel == PagedAttendPlan::kPrompt ? (size_t)paged_prompt_tiles(d.G, n_reqs, total_q) * d.Hkv : 0;
   p.q_factors = p.q_pieces + up(tiles * paged_prompt_tile_bytes(d.D));
   p.cuts = p.q_factors + up(tiles * (paged_prompt_rows() / 2) * sizeof(float));
-  p.total = p.cuts + (p.kernel == PagedAttendPlan::kPrompt ? up((size_t)p.grid * 32) : 0);
+  p.total = p.cuts + up((size_t)p.grid * 32);
   return p;
 }
 

@@ -27,9 +27,9 @@
 // is computed under this one's softmax.
 //
 // Bound by the pages' bytes.  Measured on 32/4 heads of 128: 16 contexts of 32768 tokens
-// 89 us (5.95 TB/s, 89 % of the measured copy rate), 64 of 1024 to 32768 with masses 190 us;
-// one of 131072 on 64/8 heads 51 us (5.2 TB/s), where about 4 us before the first copy
-// and the join weigh more; one of 700 tokens 8 us.
+// 89 us (5.95 TB/s, 89 % of the measured copy rate), 64 of 1024 to 32768 with masses 187 us;
+// one of 131072 on 64/8 heads 52 us (5.2 TB/s), where about 4 us before the first copy
+// and the join weigh more; one of 700 tokens 10 us, the call included.
 #include "paged_mma.cuh"
 
 namespace kvs {
@@ -101,29 +101,18 @@ struct Walk {
   }
 };
 
-// Sum over the requests of their units' tiles, and the prefix before `upto`, by every thread
-// of a block of `threads` (a multiple of 32, at most 256).
-__device__ void total_tiles(const PagedAttend& a, int upto, int threads, long long* s_sum,
-                            long long& total, long long& before) {
-  long long all = 0, pre = 0;
-  for (int r = threadIdx.x; r < a.n_reqs; r += threads) {
-    const int t = unit_of(a, r).tiles;
-    all += t;
-    if (r < upto) pre += t;
-  }
+// Tiles of the call, by every thread of the block.
+__device__ long long total_tiles(const PagedAttend& a, long long* s_sum) {
+  long long all = 0;
+  for (int r = threadIdx.x; r < a.n_reqs; r += kThreads) all += unit_of(a, r).tiles;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    pre += __shfl_xor_sync(0xffffffffu, pre, o);
-  }
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) { s_sum[warp] = all; s_sum[8 + warp] = pre; }
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = all;
   __syncthreads();
-  total = before = 0;
-  for (int w = 0; w < threads / 32; ++w) { total += s_sum[w]; before += s_sum[8 + w]; }
+  all = 0;
+  for (int w = 0; w < kThreads / 32; ++w) all += s_sum[w];
   __syncthreads();
-  total *= a.d.Hkv;
-  before *= a.d.Hkv;
+  return all * a.d.Hkv;
 }
 
 template <int D, int RT>
@@ -147,7 +136,7 @@ struct Misc {
   uint32_t tmem;
   int token[32];         // query token of a row
   int start_r, start_h, start_t;
-  long long sums[16];
+  long long sums[kThreads / 32];
   float ks[6][kTileBlocks], ev[6][kTileBlocks], iv[6][kTileBlocks];   // of each stage's blocks
   float qc[2][32];
   float wmax[2][4][32];
@@ -192,10 +181,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
   }
   // this CTA's range: kThreads requests at a time (a call of more has their tiles counted first)
   long long total = 0, base = 0;
-  if (a.n_reqs > kThreads) {
-    long long unused;
-    total_tiles(a, 0, kThreads, ms.sums, total, unused);
-  }
+  if (a.n_reqs > kThreads) total = total_tiles(a, ms.sums);
   long long begin = 0, end = 0;
   for (int r0 = 0; r0 < a.n_reqs; r0 += kThreads) {
     const int r = r0 + tid;
@@ -235,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
   __syncthreads();
   umma::fence_after();
   if (begin >= end) {                        // more CTAs than tiles
+    if (tid == 0) a.cuts[blockIdx.x * 8 + 2] = 0;
     if (warp == 5) umma::dealloc(ms.tmem, C::TMEM);
     return;
   }
@@ -411,6 +398,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
       if (lane == 0) mbar_arrive(smem_u32(&ms.q_ready));
     };
     load_q(w, 0);
+    if (tid == 127) {
+      // the unit that this share enters in its middle, if that is the unit's first cut, and the CTAs that have a
+      // part of it: [blockIdx.x - 1, last], the first of them in its slot 1 unless the unit is its first
+      const long long ctas = min((long long)gridDim.x, total), before = total * (blockIdx.x - 1ll) / ctas;
+      const long long off = begin - w.t0;
+      const bool first = w.t0 > 0 && before <= off;
+      const int last = first ? cta_of(off + w.u.tiles - 1, total, (int)ctas) : 0;
+      *reinterpret_cast<int4*>(a.cuts + blockIdx.x * 8) = make_int4(w.r, w.h, last, off > before);
+    }
     named_sync(1, 128);                                    // qc of all rows
     int count = 0, seg = 0;
     bool ok = true;
@@ -577,67 +573,72 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
   }
 }
 
-// CTA of `ctas` <= total that holds tile x of `total`: the last one that begins at or before it.
-__device__ __forceinline__ int cta_of(long long x, long long total, int ctas) {
-  return (int)(((x + 1) * ctas + total - 1) / total) - 1;
-}
-
-// Adds the partials of the units that a cut splits: a CTA per (unit, row), a thread to a
-// dimension and every (256 / D)th part.
-constexpr int kJoinThreads = 256, kMostParts = 1024;
+// Adds the partials of the unit that CTA blockIdx.x + 1 left in its cut (most CTAs cut none, and their
+// blocks here end at once).  Two rows to a block; a warp has a row and every fourth part, a lane four dimensions.
+constexpr int kJoinRows = 2, kJoinGroups = 4, kJoinThreads = kJoinRows * kJoinGroups * 32;
 template <int D, int RT, bool MASS>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttend a, const int grid) {
-  __shared__ long long sums[16];
-  __shared__ float weight[kMostParts];
-  __shared__ float acc_of[kJoinThreads];
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttend a) {
+  __shared__ float4 sums[kJoinGroups - 1][kJoinRows][D / 4];
   launch_dependents();
-  const PagedDev& d = a.d;
-  const int unit = blockIdx.x, r = unit / d.Hkv, h = unit % d.Hkv, row = blockIdx.y, tid = threadIdx.x;
-  const Unit u = unit_of(a, r);
-  const bool live = u.tiles > 0 && row < u.n * d.G;
-  int c0 = 0, n = 1;
-  size_t rec0 = 0;
-  if (live) {
-    long long total, before;
-    total_tiles(a, r, kJoinThreads, sums, total, before);
-    const long long off = before + (long long)h * u.tiles;
-    const int ctas = (int)min((long long)grid, total);
-    c0 = cta_of(off, total, ctas);
-    n = cta_of(off + u.tiles - 1, total, ctas) - c0 + 1;
-    rec0 = (size_t)(2 * c0 + (off > total * c0 / ctas ? 1 : 0)) * RT + row;   // the first CTA's: maybe not its first unit
-  }
   wait_previous();
-  if (!live || n == 1) return;
-  auto rec_of = [&](int i) { return i == 0 ? rec0 : (size_t)(2 * (c0 + i)) * RT + row; };
-  // every warp finds the maximum and the sum; the parts' weights go to shared memory
+  const PagedDev& d = a.d;
+  const int4 cut = *reinterpret_cast<const int4*>(a.cuts + (blockIdx.x + 1) * 8);
+  const int r = cut.x, h = cut.y, c0 = blockIdx.x, n = cut.z - c0 + 1;
+  if (cut.z == 0) return;
+  const Unit u = unit_of(a, r);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kJoinRows, group = warp / kJoinRows;
+  const int row = blockIdx.y * kJoinRows + mine;
+  const bool live = row < u.n * d.G;
+  auto rec_of = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? cut.w : 0)) * RT + row; };
   float top = -INFINITY, sum = 0.f;
-  for (int i = tid & 31; i < n; i += 32) top = fmaxf(top, a.part_ml[rec_of(i)].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_ml[rec_of(i)].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float ref = top > -INFINITY ? top : 0.f;
-  for (int i = tid & 31; i < n; i += 32) {
-    const float2 ml = a.part_ml[rec_of(i)];
-    const float f = ex2(ml.x - ref);
-    sum = fmaf(ml.y, f, sum);
-    if (tid < 32) weight[i] = f;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  __syncthreads();
-  float acc = 0.f;
-  const int dim = tid % D;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top > -INFINITY ? top : 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float f = 0.f;                         // the weight of part i0 + lane
+      if (i0 + lane < n) {
+        const float2 ml = a.part_ml[rec_of(i0 + lane)];
+        f = ex2(ml.x - ref);
+        sum = fmaf(ml.y, f, sum);
+      }
+      const int most = min(32, n - i0);
 #pragma unroll 8
-  for (int i = tid / D; i < n; i += kJoinThreads / D) acc = fmaf(a.part_o[rec_of(i) * D + dim], weight[i], acc);
-  acc_of[tid] = acc;
-  __syncthreads();
-  const int hq = h * d.G + row % d.G;
-  if (tid < D) {
+      for (int i = group; i < most; i += kJoinGroups) {
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        if (lane < D / 4) {
+          const float4 v = reinterpret_cast<const float4*>(a.part_o + rec_of(i0 + i) * D)[lane];
+          acc.x = fmaf(v.x, w, acc.x);
+          acc.y = fmaf(v.y, w, acc.y);
+          acc.z = fmaf(v.z, w, acc.z);
+          acc.w = fmaf(v.w, w, acc.w);
+        }
+      }
+    }
 #pragma unroll
-    for (int k = 1; k < kJoinThreads / D; ++k) acc += acc_of[tid + k * D];
-    static_cast<__nv_bfloat16*>(a.out)[((size_t)(u.first + row / d.G) * d.Hq + hq) * D + tid] =
-        __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (group > 0 && lane < D / 4) sums[group - 1][mine][lane] = acc;
   }
-  if (MASS && tid == 0) a.lse[(size_t)r * d.Hq + hq] = top + log2f(sum);
+  __syncthreads();
+  if (!live || group > 0) return;
+  const int hq = h * d.G + row % d.G;
+  if (lane < D / 4) {
+#pragma unroll
+    for (int g = 1; g < kJoinGroups; ++g) {
+      const float4 v = sums[g - 1][mine][lane];
+      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    uint2 raw;
+    raw.x = *reinterpret_cast<const uint32_t*>(&lo);
+    raw.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + ((size_t)(u.first + row / d.G) * d.Hq + hq) * D + lane * 4) = raw;
+  }
+  if (MASS && lane == 0) a.lse[(size_t)r * d.Hq + hq] = top + log2f(sum);
 }
 
 template <int D, int RT, bool MASS>
@@ -646,13 +647,12 @@ cudaError_t launch(const PagedAttend& a, int grid, cudaStream_t st) {
   static std::atomic<unsigned long long> opted{0};
   cudaError_t e = smem_optin_once(opted, decode_kernel<D, RT, MASS>, C::SMEM);
   if (e != cudaSuccess) return e;
-  if (grid > kMostParts) return cudaErrorInvalidConfiguration;
   decode_kernel<D, RT, MASS><<<grid, kThreads, C::SMEM, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  const int rows = a.max_q_len * a.d.G;
-  cfg.gridDim = dim3(a.n_reqs * a.d.Hkv, rows);
+  cfg.gridDim = dim3(grid - 1, (a.max_q_len * a.d.G + kJoinRows - 1) / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -660,7 +660,7 @@ cudaError_t launch(const PagedAttend& a, int grid, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, RT, MASS>, a, grid);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, RT, MASS>, a);
 }
 
 template <int D>

@@ -185,6 +185,12 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// CTA of `ctas` <= total that holds tile x of `total`: the last one that begins at or before it, where CTA c begins at
+// total * c / ctas.
+__device__ __forceinline__ int cta_of(long long x, long long total, int ctas) {
+  return (int)(((x + 1) * ctas + total - 1) / total) - 1;
+}
+
 // Let the next kernel of the stream start; wait for the previous one's results.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

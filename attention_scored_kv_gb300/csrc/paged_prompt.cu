@@ -232,12 +232,6 @@ struct Walk {
   }
 };
 
-// The unit that CTA c's share enters in its middle, if that is the unit's first cut: the unit and the CTAs
-// [c - 1, last] that have a part of it.  The CTA before is in its slot 1 unless the unit is its first.
-struct Cut {
-  int r, qg, h, last, slot;                // last 0: none
-};
-
 struct Misc {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], drain;
   uint64_t s_ready[2], p_ready[2], o_done[2];
@@ -423,24 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
   const long long ctas = min((long long)gridDim.x, total);
   if (blockIdx.x >= ctas) {
     if (tid == 0) a.cuts[blockIdx.x * 8 + 3] = 0;
+    wait_previous();                         // nothing that follows runs before the split queries are done with
     return;
   }
   const long long begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
   locate(a, per, kThreads / 32, begin, search);
-  if (tid == 0) {
-    const int c = blockIdx.x;
-    const long long off = begin - search.t;               // the unit's start
-    Cut cut{search.r, search.qg, search.h, 0, 0};
-    if (search.t > kSetup && total * (c - 1) / ctas <= off + kSetup) {
-      const Unit u = unit_of(a, req_of(a, cut.r), cut.qg, per);
-      cut.last = c;
-      while (cut.last + 1 < ctas && total * (cut.last + 1) / ctas < off + u.cost()) ++cut.last;
-      cut.slot = off > total * (c - 1) / ctas;
-    }
-    int* at = a.cuts + c * 8;
-    at[0] = cut.r; at[1] = cut.qg; at[2] = cut.h; at[3] = cut.last; at[4] = cut.slot;
-  }
-
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(smem_u32(&ms.k_full[i]), 1);
@@ -555,6 +536,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
     for (int i = max(0, w.seg - kQStages); i < w.seg; ++i) mbar_wait(smem_u32(&ms.q_ready[i % kSlots]), (i / kSlots) & 1);
   } else if (warp == kQWarp + 1) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
+    // ---- for the join kernel: the unit that this share enters in its middle, if that is the unit's first cut, and
+    // the CTAs that have a part of it: [blockIdx.x - 1, last], the first in its slot 1 unless the unit is its first
+    if (lane == 0) {
+      const long long before = total * (blockIdx.x - 1ll) / ctas, off = begin - w.v0;     // the unit's start
+      const bool first = w.v0 > kSetup && before <= off + kSetup;
+      int* at = a.cuts + blockIdx.x * 8;
+      at[0] = w.r;
+      at[1] = w.qg;
+      at[2] = w.h;
+      at[3] = first ? cta_of(off + w.u.cost() - 1, total, (int)ctas) : 0;
+      at[4] = off > before;
+    }
   } else if (warp >= kVWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
     // ---- V: a page's row d (16 tokens of a dimension) becomes two 16-byte operand rows
@@ -821,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
 }
 
 // Adds the partials of the unit that CTA blockIdx.x + 1 left in its cut.
-constexpr int kJoinThreads = 256, kJoinRows = 16;
+constexpr int kJoinThreads = 256, kJoinRows = 16, kMostParts = 256;   // a part per CTA at most
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAttend a, const int qpt) {
   wait_previous();
@@ -831,22 +824,44 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAt
   if (c1 == 0) return;
   const Req q = req_of(a, r);
   const Unit u = unit_of(a, q, qg, 2 * qpt);
+  __shared__ float weight[kMostParts][kJoinRows + 1], total[kJoinRows];
+  const int n = c1 - c0 + 1;
+  auto rec_of = [&](int x, int i) { return ((size_t)(2 * (c0 + i) + (i == 0 ? slot : 0)) * 2 + x) * kRows; };
+  // 16 threads to a row find its parts' weights and its sum
+  {
+    const int mine = threadIdx.x / 16, idx = threadIdx.x % 16, pr = blockIdx.y * kJoinRows + mine;
+    const int x = pr / kRows, row = pr % kRows;
+    const int parts = row / d.G < qpt && x * qpt + row / d.G < u.cnt ? n : 0;    // a warp has two rows: the
+    float top = -INFINITY, sum = 0.f;                                            // shuffles are for both
+    for (int i = idx; i < parts; i += 16) top = fmaxf(top, a.part_ml[rec_of(x, i) + row].x);
+    __syncwarp();
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o, 16));
+    const float ref = top > -INFINITY ? top : 0.f;
+    for (int i = idx; i < parts; i += 16) {
+      const float2 ml = a.part_ml[rec_of(x, i) + row];
+      const float f = ex2(ml.x - ref);
+      sum = fmaf(ml.y, f, sum);
+      weight[i][mine] = f;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
+    if (idx == 0) total[mine] = sum;
+  }
+  __syncthreads();
   // a thread has four dimensions of a row; partials are [tile][D / 4][128 rows][4]
   const int pr = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, x = pr / kRows, row = pr % kRows;
   const int i = x * qpt + row / d.G;
   if (row / d.G >= qpt || i >= u.cnt) return;
-  auto rec_of = [&](int e) { return ((size_t)(2 * e + (e == c0 ? slot : 0)) * 2 + x) * kRows; };
-  float top = -INFINITY, sum = 0.f;
-  for (int e = c0; e <= c1; ++e) top = fmaxf(top, a.part_ml[rec_of(e) + row].x);
-  const float ref = top > -INFINITY ? top : 0.f;
+  const float sum = total[threadIdx.x % kJoinRows];
   float4 acc[D / 64];
 #pragma unroll
   for (int q4 = 0; q4 < D / 64; ++q4) acc[q4] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int e = c0; e <= c1; ++e) {
-    const size_t rec = rec_of(e);
-    const float2 ml = a.part_ml[rec + row];
-    const float f = ex2(ml.x - ref);
-    sum = fmaf(ml.y, f, sum);
+#pragma unroll 4
+  for (int e = 0; e < n; ++e) {
+    const size_t rec = rec_of(x, e);
+    const float f = weight[e][threadIdx.x % kJoinRows];
 #pragma unroll
     for (int q4 = 0; q4 < D / 64; ++q4) {
       const float4 v = reinterpret_cast<const float4*>(a.part_o)[rec * (D / 4) + (threadIdx.x / kJoinRows + 16 * q4) * kRows + row];
@@ -876,6 +891,7 @@ cudaError_t launch_d(const PagedAttend& a, int grid, cudaStream_t st) {
   static std::atomic<unsigned long long> opted{0};
   cudaError_t e = smem_optin_once(opted, prompt_kernel<D>, C::SMEM);
   if (e != cudaSuccess) return e;
+  if (grid > kMostParts) return cudaErrorInvalidConfiguration;
   const int qpt = kRows / a.d.G;
   split_kernel<D><<<dim3(paged_prompt_tiles(a.d.G, a.n_reqs, a.total_q), a.d.Hkv), kRows, 0, st>>>(a, qpt);
   e = cudaGetLastError();
