@@ -352,10 +352,12 @@ def run(s):
         if op == "gather":
             return s.cache.gather(0, s.read)
         if s.case["scored"]:
-            return {"out": s.cache.attend(0, s.q, s.table, s.kv_len, block_mass=s.mass), "mass": s.mass}
+            return {"out": s.cache.attend(0, s.q, s.table, s.kv_len, window=s.case["window"], block_mass=s.mass),
+                    "mass": s.mass}
         if s.max_new == 1:
-            return s.cache.attend(0, s.q, s.table, s.kv_len)
-        return s.cache.attend(0, s.q, s.table, s.kv_len, q_start=s.q_start, max_q_len=s.max_new)
+            return s.cache.attend(0, s.q, s.table, s.kv_len, window=s.case["window"])
+        return s.cache.attend(0, s.q, s.table, s.kv_len, q_start=s.q_start, max_q_len=s.max_new,
+                              window=s.case["window"])
     if op == "plan":
         return _plan(s)
     if op == "append":
