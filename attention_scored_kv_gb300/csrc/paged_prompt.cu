@@ -5,22 +5,26 @@
 // tiles A and B of 128), which share every K and V they read.  Per 128 cached tokens:
 //   S = Q K^T        two pieces of Q (4 significant bits each) as one contraction of 2 D,
 //                    E4M3 x E4M3, K as it is stored
-//   t = S kscale c_r + log2 vscale,  m_r: a reference at or below the row's maximum so far
-//   x = 2^(t - m_r),  l_r += x / vscale,  O += X V      f16 x f16
+//   t = S kscale c_r + log2 vscale,  m_r: the t of some token that the row has seen
+//   x = 2^(t - m_r) rounded to bf16,  l_r += x / vscale,  O += X V      bf16 x bf16
 // and o = O / l.  The scales are powers of two, so V's rides in x's exponent and V's codes
-// are exact in f16.  m moves only when a row passes it by 2^15 (x still fits f16, whose 11 bits
-// are finer than the output's 8), which is seen from the sums that l needs anyway; O is
-// then rescaled.  Queries: exact down to 2^-10 of the row's largest element, an error of
-// 2^-19 of the largest below that.
+// are exact in bf16.  x is rounded to 8 bits as the output is, and l sums the rounded x, so that a
+// row of one strong token has no error from it (with l of the exact x the whole error was up to
+// 1.43 times that of rounding the output alone, so 1.19; the exact l would be 4 % faster).  bf16 has
+// float32's exponents, so m need not follow the maximum: it moves, and O is rescaled, only where x would pass
+// 2^63 or l leave float32.  With x in f16, whose 2^16 strong tokens passed in every third half tile of
+// the 8192-token prompt, the exponentials taken again and O rescaled cost it 16 %.
+// Queries: exact down to 2^-10 of the row's largest element, an error of 2^-19 of the largest below that.
 //
 // How: work is cut as in the decode kernel: the 128-token tiles of all units laid end to
 // end and split evenly over one CTA per SM, partials of split units added by a join
 // kernel.  That also balances causal rows, whose units differ in length, and feeds all
-// SMs when rows are few and the context is long.  A unit's start counts as two tiles.
+// SMs when rows are few and the context is long.  A unit's start counts as three tiles (with two
+// the CTA of the 8192-token prompt's shortest units ends last, 4 % later; four are 1 % slower).
 // A split kernel first writes the queries' pieces in operand layout (a few percent of the
 // time; two warps of each CTA that did it took 15 to 27 thousand clocks a unit).
 // Per CTA: one warp copies K pages into a ring, one the queries, four convert V's codes to
-// f16 operand rows (a page's rows are its operand rows, so it is load, convert, store), one
+// bf16 operand rows (a page's rows are its operand rows, so it is load, convert, store), one
 // issues the matrix instructions, and two groups of four warps do the softmax of A and B, a
 // thread to a row, so that no row statistic crosses threads.  The matrix warp works on
 // one tile while the other's softmax runs: O(A) += X(A, j) V and S(A, j+1) while B's
@@ -28,11 +32,14 @@
 // first operand: from shared memory the two operands of both products, X's stores and V's
 // would be 368 KB a step, 2900 clocks at 128 bytes, against the tensor core's 2048.
 //
-// Bound by the chain of one tile: softmax (1300 to 1500 clocks), X's store (200), its two
-// products (1300), of which only the other tile's overlap: about 4000 clocks a step of 128
-// tokens, against 2048 of matrix work.  Measured on 32/4 heads of 128: an 8192-token
-// prompt 525 us (1.05 PFLOP/s, 55 % of the measured bf16 rate), five chunks of 100 to 2048
-// tokens behind up to 8192 397 us (945 TFLOP/s).
+// P is handed over in halves of 64 tokens: the first one's product runs under the second one's
+// exponentials, and the half that a thread holds fits its registers.
+//
+// Bound by the chain of one tile (two halves' exponentials, X's stores, the second half's product and the
+// next S), which only the other tile's overlaps: 3200 clocks a step of 128 tokens, against 2048 of matrix work,
+// 56 % of the tensor core's time.  Measured on 32/4 heads of 128: an 8192-token prompt 465 us
+// (1.18 PFLOP/s, 62 % of the measured bf16 rate), five chunks of 100 to 2048 tokens behind up to
+// 8192 333 us (1.13 PFLOP/s).
 #include "paged_mma.cuh"
 
 namespace kvs {
@@ -47,12 +54,14 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10, kVWarp = 12, kVThreads =
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 constexpr int kKStages = 3, kVStages = 2, kQStages = 1;
 constexpr int kSlots = 4;                // scales of this many tiles, row factors of this many segments
-constexpr int kSetup = 2;                // what a unit's start costs, in tiles, where work is cut
+constexpr int kSetup = 3;                // what a unit's start costs, in tiles, where work is cut
 constexpr int kRows = 128;               // rows of a tile of queries
 constexpr int kChunk = 512;              // requests of one round of the search
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 15.f;           // the maximum moves when a row passes it by this: x <= 2^15 fits f16
-constexpr float kLimit = 32768.f;        // 2^kSlack: more in a block's sum, and the maximum is looked at
+// A row's reference moves where x would pass 2^kFarX or a part of l 2^kFarL.  What passes kLimit shows it: half a
+// tile's part of l, and a block's sum of x times kSumShare.  Sums of 2^26 tokens then stay within float32.
+constexpr float kFarX = 63.f, kFarL = 99.f;
+constexpr float kLimit = 0x1p106f, kSumShare = 0x1p38f;
 
 // Units of request r: groups of `per` query tokens, all KV heads alike.
 struct Req {
@@ -234,7 +243,7 @@ struct Walk {
 
 struct Misc {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], drain;
-  uint64_t s_ready[2], p_ready[2], o_done[2];
+  uint64_t s_ready[2], p_ready[2][2], half_done[2], o_done[2];
   uint64_t q_ready[kSlots], q_empty[kQStages], sc_ready[kSlots];
   uint32_t tmem;
   alignas(16) float ks[kSlots][kTileBlocks], vs[kSlots][kTileBlocks];
@@ -249,94 +258,131 @@ struct Cfg {
   static constexpr int PAGE = 16 * D;
   static constexpr int Q = kRows * 2 * D;                 // one tile of queries, both pieces
   static constexpr int K = kTileBlocks * PAGE;            // a stage of K
-  static constexpr int V = kTile * D * 2;                 // V as f16
+  static constexpr int V = kTile * D * 2;                 // V as bf16
   static constexpr int BODY = kQStages * 2 * Q + kKStages * K + kVStages * V;
   static constexpr int SMEM = BODY + (int)sizeof(Misc) + 1024;
   static_assert(SMEM + (int)sizeof(Search) <= 227 * 1024, "shared memory");
 };
 
-// What a row's thread needs of a tile of 128 tokens: the blocks' scales and what it sees.
-struct Tile {
-  float ks[kTileBlocks], vs[kTileBlocks];  // in registers: the operands' traffic starves shared-memory loads
-  uint32_t seen[4];      // where the tile is masked: the tokens that the row sees, as bits
-  __device__ __forceinline__ bool hidden(int k) const { return !(seen[k >> 5] >> (k & 31) & 1); }
-  __device__ __forceinline__ void look(int base, int lo, int hi, uint32_t bad) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int up = hi - base - 32 * j, down = lo - base - 32 * j;      // sees bits [down, up)
-      uint32_t v = up >= 32 ? ~0u : up <= 0 ? 0u : (1u << up) - 1;
-      v &= down <= 0 ? ~0u : down >= 32 ? 0u : ~0u << down;
-      if (bad >> (2 * j) & 1) v &= 0xffff0000u;
-      if (bad >> (2 * j + 1) & 1) v &= 0xffffu;
-      seen[j] = v;
-    }
-  }
-  __device__ __forceinline__ float ev(int b) const { return (float)((__float_as_int(vs[b]) >> 23) - 127); }
-  __device__ __forceinline__ float iv(int b) const { return __int_as_float((254 << 23) - __float_as_int(vs[b])); }
+// The scales of half a tile, 64 tokens, in registers: the operands' traffic starves shared-memory loads.
+constexpr int kHalf = kTile / 2, kHalfBlocks = kTileBlocks / 2;
+__device__ __forceinline__ float scale_log2(float s) { return (float)((__float_as_int(s) >> 23) - 127); }
+__device__ __forceinline__ float scale_inverse(float s) { return __int_as_float((254 << 23) - __float_as_int(s)); }
+struct Half {
+  float ks[kHalfBlocks], vs[kHalfBlocks];
+  __device__ __forceinline__ float ev(int b) const { return scale_log2(vs[b]); }
+  __device__ __forceinline__ float iv(int b) const { return scale_inverse(vs[b]); }
 };
 
-// The largest t of the row's tokens.
-template <bool MASK>
-__device__ __forceinline__ float row_max(uint32_t t_s, const Tile& y, float c) {
-  float top = -INFINITY;
-  uint32_t r[2][16];
-  ld16_start(t_s, r[0]);
-#pragma unroll
-  for (int b = 0; b < kTileBlocks; ++b) {
-    ld16_wait(r[b & 1]);
-    if (b + 1 < kTileBlocks) ld16_start(t_s + 16 * (b + 1), r[(b + 1) & 1]);
-    float s[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      s[k] = __uint_as_float(r[b & 1][k]);
-      if (MASK && y.hidden(16 * b + k)) s[k] = -INFINITY;
-    }
-    float v = max3(s[0], s[1], s[2]), u = max3(s[3], s[4], s[5]);
-    v = max3(v, s[6], s[7]);
-    u = max3(u, s[8], s[9]);
-    v = max3(v, s[10], s[11]);
-    u = max3(u, s[12], s[13]);
-    v = max3(v, s[14], s[15]);
-    v = fmaxf(v, u);
-    const float tb = fmaf(v, y.ks[b] * c, y.ev(b));
-    top = fmaxf(top, MASK && v == -INFINITY ? v : tb);
-  }
-  return top;
+// lo and hi plus the two elements of v.
+__device__ __forceinline__ void add_bf16x2(float& lo, float& hi, uint32_t v) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n add.rn.f32.bf16 %0, l, %0;\n add.rn.f32.bf16 %1, h, %1;\n}"
+      : "+f"(lo), "+f"(hi) : "r"(v));
 }
 
-// x = 2^(t - ref) of the row's tokens as f16 pairs; the largest sum of a block to `big`.
+// x = 2^(t - ref) of the row's half of a tile, as bf16 pairs; the largest sum of a block to `most`.
 // Returns the row's part of l.
-template <bool MASK>
-__device__ __forceinline__ float row_exp(uint32_t t_s, const Tile& y, float c, float ref, uint32_t (&h)[64], float& big) {
+__device__ __forceinline__ float row_exp(uint32_t t_s, const Half& y, float c, float ref, uint32_t (&h)[32], float& most) {
   float l = 0.f;
-  big = 0.f;
-  uint32_t r[2][16];
-  ld16_start(t_s, r[0]);
+  most = 0.f;
+  uint32_t r[2][32];
+  ld32_start(t_s, r[0]);
 #pragma unroll
-  for (int b = 0; b < kTileBlocks; ++b) {
-    ld16_wait(r[b & 1]);
-    if (b + 1 < kTileBlocks) ld16_start(t_s + 16 * (b + 1), r[(b + 1) & 1]);
+  for (int b = 0; b < kHalfBlocks; ++b) {
+    uint32_t* v = r[b / 2 & 1] + b % 2 * 16;
+    if (b % 2 == 0) {
+      ld32_wait(r[b / 2 & 1]);
+      if (b + 2 < kHalfBlocks) ld32_start(t_s + 16 * (b + 2), r[(b / 2 + 1) & 1]);
+    }
     const float m1 = y.ks[b] * c, s1 = y.ev(b) - ref;
     const uint64_t mul = pack2(m1, m1), sub = pack2(s1, s1);
-    uint64_t sum0 = 0, sum1 = 0;
+    float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float2 t = unpack2(fma2(pack2(__uint_as_float(r[b & 1][2 * k]), __uint_as_float(r[b & 1][2 * k + 1])), mul, sub));
-      float x0 = ex2(t.x), x1 = ex2(t.y);
-      if (MASK) {
-        if (y.hidden(16 * b + 2 * k)) x0 = 0.f;
-        if (y.hidden(16 * b + 2 * k + 1)) x1 = 0.f;
-      }
-      if (k & 1) sum1 = add2(sum1, pack2(x0, x1)); else sum0 = add2(sum0, pack2(x0, x1));
-      const __half2 p = __floats2half2_rn(x0, x1);
-      h[8 * b + k] = *reinterpret_cast<const uint32_t*>(&p);
+      const float2 t = unpack2(fma2(pack2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), mul, sub));
+      const float x0 = ex2(t.x), x1 = ex2(t.y);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(x0, x1);
+      const uint32_t q = h[8 * b + k] = *reinterpret_cast<const uint32_t*>(&p);
+      add_bf16x2(sum0, sum1, q);
     }
-    const float2 f = unpack2(add2(sum0, sum1));
-    const float s = f.x + f.y;
-    big = fmaxf(big, s);
+    const float s = sum0 + sum1;
+    most = fmaxf(most, s);
     l = fmaf(s, y.iv(b), l);
   }
   return l;
+}
+
+// The tokens of a block of 16 at position `pos` that a row sees, as bits.
+__device__ __forceinline__ uint32_t seen_of(int pos, int lo, int hi) {
+  const int up = min(max(hi - pos, 0), kBlock), down = min(max(lo - pos, 0), kBlock);
+  return (1u << up) - (1u << min(up, down));
+}
+
+// Half a tile in general: rows that do not see all of it, that have seen nothing yet, or whose x is out of range.
+// Looks at the maxima first and moves a reference where it has to.  Writes x to TMEM over the half's S.  A loop, apart
+// from row_exp: few halves come here, and one loop with both forms cost the others 13 % in registers and moves.
+struct Row {
+  float m, f, add;
+};
+__device__ __forceinline__ void half_general(Row& w, uint32_t t_h, uint32_t t_p, const float* ks, const float* vs, float c,
+                                             int pos, int lo, int hi, uint32_t gone) {
+  float top = -INFINITY, top_l = -INFINITY;  // of x's and of l's logarithms
+#pragma unroll 1
+  for (int b = 0; b < kHalfBlocks; b += 2) {
+    uint32_t s[32];
+    ld32_start(t_h + 16 * b, s);
+    ld32_wait(s);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t seen = gone >> (b + e) & 1 ? 0u : seen_of(pos + 16 * (b + e), lo, hi);
+      float v = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v = fmaxf(v, seen >> k & 1 ? __uint_as_float(s[16 * e + k]) : -INFINITY);
+      if (v > -INFINITY) {
+        top = fmaxf(top, fmaf(v, ks[b + e] * c, scale_log2(vs[b + e])));
+        top_l = fmaxf(top_l, v * (ks[b + e] * c));
+      }
+    }
+  }
+  w.f = 1.f;                                 // what O and l so far are to be scaled by
+  if (top > w.m + kFarX || top_l > w.m + kFarL || (w.m == -INFINITY && top > -INFINITY)) {
+    w.f = w.m == -INFINITY ? 0.f : ex2(w.m - top);
+    w.m = top;
+  }
+  const float ref = w.m == -INFINITY ? 0.f : w.m;
+  w.add = 0.f;
+#pragma unroll 1
+  for (int b = 0; b < kHalfBlocks; b += 2) {
+    uint32_t s[32], h[16];
+    ld32_start(t_h + 16 * b, s);
+    ld32_wait(s);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t seen = gone >> (b + e) & 1 ? 0u : seen_of(pos + 16 * (b + e), lo, hi);
+      const float m1 = ks[b + e] * c, s1 = scale_log2(vs[b + e]) - ref;
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = 16 * e + 2 * k;
+        float x0 = ex2(fmaf(__uint_as_float(s[i]), m1, s1)), x1 = ex2(fmaf(__uint_as_float(s[i + 1]), m1, s1));
+        if (!(seen >> (2 * k) & 1)) x0 = 0.f;
+        if (!(seen >> (2 * k + 1) & 1)) x1 = 0.f;
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x0, x1);
+        sum += __low2float(p) + __high2float(p);
+        h[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      w.add = fmaf(sum, scale_inverse(vs[b + e]), w.add);
+    }
+    st16(t_p + 8 * b, reinterpret_cast<const float*>(h));
+    wait_st();                               // the second half's S is read after the first's x is written
+  }
+}
+
+// Exact: 4 significant bits.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t c) {
+  const float2 f = __half22float2(e4m3x2_to_half2(c));
+  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // Place of a tile of queries among the split ones, from its first packed row: a request's tiles are
@@ -434,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
     mbar_init(smem_u32(&ms.drain), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms.s_ready[i]), 1);
-      mbar_init(smem_u32(&ms.p_ready[i]), 4);
+      mbar_init(smem_u32(&ms.p_ready[i][0]), 4);
+      mbar_init(smem_u32(&ms.p_ready[i][1]), 4);
+      mbar_init(smem_u32(&ms.half_done[i]), 1);
       mbar_init(smem_u32(&ms.o_done[i]), 1);
       mbar_init(smem_u32(&ms.q_empty[i]), 1);
     }
@@ -585,8 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
           uint32_t h[8];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * u]) : "h"((uint16_t)(c[u] & 0xffffu)));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * u + 1]) : "h"((uint16_t)(c[u] >> 16)));
+            h[2 * u] = e4m3x2_to_bf16x2(c[u] & 0xffffu);
+            h[2 * u + 1] = e4m3x2_to_bf16x2(c[u] >> 16);
           }
           uint4* dst = reinterpret_cast<uint4*>(sv + st * C::V + (size_t)(2 * (i * PPI + pp)) * (D * 16) + dim * 16);
           dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
@@ -606,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
   } else if (warp == kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
     // ---- matrix instructions
-    constexpr uint32_t id_qk = idesc_e4m3(128, 128), id_pv = umma::idesc_f16(false, 128, D);
+    constexpr uint32_t id_qk = idesc_e4m3(128, 128), id_pv = umma::idesc_f16(true, 128, D);
     const uint32_t on = elect();
     int count = 0, count_b = 0;
     bool ok = true;
@@ -619,13 +667,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
                  id_qk, k > 0);
       commit(on, smem_u32(&ms.s_ready[x]));
     };
-    auto pv = [&](int x, int n, bool fresh, bool last) {  // O of tile x with V number n
+    auto pv = [&](int x, int n, int half, bool fresh) {   // O of tile x with half of V number n
       const uint32_t bv = desc_lo(smem_u32(sv + (n % kVStages) * C::V), D * 16);
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_f16_ts(on, tmem + 256 + x * 128, tmem + x * 128 + k * 8, bv + k * (2 * D), desc_hi(128), id_pv,
-                   !(fresh && k == 0));
+      for (int k = 0; k < kHalf / 16; ++k)
+        mma_f16_ts(on, tmem + 256 + x * 128, tmem + x * 128 + half * (kHalf / 2) + k * 8,
+                   bv + (half * (kHalf / 16) + k) * (2 * D), desc_hi(128), id_pv, !(fresh && k == 0));
+    };
+    // a tile's products as the halves of its P come
+    auto products = [&](int x, int n, uint32_t parity, bool first, bool last) {
+      ok = ok && warp_wait(smem_u32(&ms.p_ready[x][0]), parity);
+      if (!ok) return;
+      umma::fence_after();
+      pv(x, n, 0, first);
+      commit(on, smem_u32(&ms.half_done[x]));
+      ok = warp_wait(smem_u32(&ms.p_ready[x][1]), parity);
+      if (!ok) return;
+      umma::fence_after();
+      pv(x, n, 1, false);                                 // before the next S, which overwrites P
       if (last) commit(on, smem_u32(&ms.o_done[x]));
+      else qk(x, n + 1);
     };
     while (w.nt > 0 && ok) {
       const bool two = w.u.cnt > qpt;
@@ -642,19 +703,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
         const int n = count + 1;
         ok = warp_wait(smem_u32(&ms.v_full[count % kVStages]), (count / kVStages) & 1);
         if (more) ok = ok && warp_wait(smem_u32(&ms.k_full[n % kKStages]), (n / kKStages) & 1);
-        ok = ok && warp_wait(smem_u32(&ms.p_ready[0]), count & 1);
+        products(0, count, count & 1, t == 0, !more);
+        if (two) products(1, count, count_b++ & 1, t == 0, !more);
         if (!ok) break;
-        umma::fence_after();
-        pv(0, count, t == 0, !more);                      // before the next S, which overwrites P
-        if (more) qk(0, n);
-        if (two) {
-          ok = warp_wait(smem_u32(&ms.p_ready[1]), count_b & 1);
-          if (!ok) break;
-          ++count_b;
-          umma::fence_after();
-          pv(1, count, t == 0, !more);
-          if (more) qk(1, n);
-        }
         commit(on, smem_u32(&ms.v_empty[count % kVStages]));
         if (more) commit(on, smem_u32(&ms.k_empty[n % kKStages]));
         if (t + 2 == w.nt) commit(on, smem_u32(&ms.q_empty[w.seg % kQStages]));
@@ -706,60 +757,61 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
           c = ms.qc[w.seg % kSlots][x * kRows + row];
         }
         ok = ok && warp_wait(smem_u32(&ms.sc_ready[slot]), ((tile + t) / kSlots) & 1);
-        Tile y;
-        *reinterpret_cast<float4*>(y.ks) = *reinterpret_cast<const float4*>(ms.ks[slot]);
-        *reinterpret_cast<float4*>(y.ks + 4) = *reinterpret_cast<const float4*>(ms.ks[slot] + 4);
-        *reinterpret_cast<float4*>(y.vs) = *reinterpret_cast<const float4*>(ms.vs[slot]);
-        *reinterpret_cast<float4*>(y.vs + 4) = *reinterpret_cast<const float4*>(ms.vs[slot] + 4);
         const uint32_t bad = ms.bad[slot];
-        const bool masked = base < all_lo || base + kTile > all_hi || bad;
-        if (masked) y.look(base, lo, hi, bad);
         if (t > 0) ok = ok && warp_wait(smem_u32(&ms.s_ready[x]), count & 1);
         if (!ok) break;
         umma::fence_after();
-        uint32_t h[64];
-        float f = 1.f, add, big;
-        // Within a segment the last maximum mostly serves, so the exponentials are taken at once.  Where a
-        // block's sum passes what the slack allows, the reference moves up by log2 of it, less the 4 that 16
-        // equal terms add, and they are taken again; only where even that overflowed are the maxima looked at.
-        bool look = t == 0 || __any_sync(0xffffffffu, m == -INFINITY), last = look;
-        for (;;) {
-          if (look) {
-            const float top = masked ? row_max<true>(t_s, y, c) : row_max<false>(t_s, y, c);
-            if (top > m + kSlack || (m == -INFINITY && top > -INFINITY)) {
-              f = m == -INFINITY ? 0.f : ex2(m - top);
-              m = top;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int from = base + half * kHalf;
+          const uint32_t gone = bad >> (half * kHalfBlocks) & ((1u << kHalfBlocks) - 1);
+          const uint32_t t_h = t_s + half * kHalf, t_p = t_s + half * (kHalf / 2);      // P: two tokens to a column
+          // Mostly all rows see all of the half and the reference serves, so the exponentials are taken at once.  The
+          // first reference is any token's t: bf16 has float32's range.
+          bool general = from < all_lo || from + kHalf > all_hi || gone;
+          if (t + half == 0 && !general) m = fmaf(ld1(t_h), ms.ks[slot][0] * c, scale_log2(ms.vs[slot][0]));
+          general = general || __any_sync(0xffffffffu, !(fabsf(m) < 1e30f));
+          float f = 1.f, add;
+          if (!general) {
+            Half y;
+            *reinterpret_cast<float4*>(y.ks) = *reinterpret_cast<const float4*>(ms.ks[slot] + half * kHalfBlocks);
+            *reinterpret_cast<float4*>(y.vs) = *reinterpret_cast<const float4*>(ms.vs[slot] + half * kHalfBlocks);
+            uint32_t h[32];
+            float most;
+            add = row_exp(t_h, y, c, m, h, most);
+            general = __any_sync(0xffffffffu, !(fmaxf(most * kSumShare, add) <= kLimit));
+            if (!general) st32(t_p, h);
+          }
+          if (general) {
+            Row r{m};
+            half_general(r, t_h, t_p, ms.ks[slot] + half * kHalfBlocks, ms.vs[slot] + half * kHalfBlocks, c, from, lo, hi,
+                         gone);
+            m = r.m;
+            f = r.f;
+            add = r.add;
+          }
+          l = fmaf(l, f, add);
+          // S was issued behind the previous tile's product, so that is done with O; the first half's may not be
+          if (t + half > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            if (half) {
+              ok = warp_wait(smem_u32(&ms.half_done[x]), count & 1);
+              if (!ok) break;
+              umma::fence_after();
+            }
+#pragma unroll
+            for (int j = 0; j < D; j += 16) {
+              float o[16];
+              ld16(t_o + j, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= f;
+              st16(t_o + j, o);
             }
           }
-          const float ref = m == -INFINITY ? 0.f : m;
-          add = masked ? row_exp<true>(t_s, y, c, ref, h, big) : row_exp<false>(t_s, y, c, ref, h, big);
-          if (last || !__any_sync(0xffffffffu, !(big <= kLimit))) break;
-          last = true;
-          look = __any_sync(0xffffffffu, !(big < 1e38f));
-          if (!look && big > kLimit) {
-            const float up = __log2f(big) - 4.f;
-            f = ex2(-up);
-            m += up;
-          }
+          wait_st();
+          umma::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready[x][half]));
         }
-        l = fmaf(l, f, add);
-        // S was issued behind the previous product, so that is done with P and O
-        if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-          for (int j = 0; j < D; j += 32) {
-            float o[32];
-            umma::ld32(t_o + j, o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= f;
-            st32(t_o + j, reinterpret_cast<const uint32_t*>(o));
-          }
-        }
-        st32(t_s, h);                                     // P over S, two tokens to a column
-        st32(t_s + 32, h + 32);
-        wait_st();
-        umma::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready[x]));
       }
       if (!ok) break;
       advance(walks[(seg + 1) & 1], w, true);

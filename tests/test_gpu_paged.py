@@ -14,12 +14,13 @@ element, with A = sum_j a_j |v_j| from the oracle and u = eps/2 of the output ty
   normalised probability is off by twice that relatively (itself and the sum), four times
   with the statistics' own rounding.
   r: what a probability is rounded to before its product with V: 2^-9 where it is kept in
-  two 8-bit pieces of 4 significant bits each, 2^-11 in f16, covered by 2^-8 for both; the
-  float32 path keeps 2^-23 (D of its roundings are in delta's term).
+  two 8-bit pieces of 4 significant bits each, 2^-9 in bf16 and as much in the sum that it is
+  divided by, covered by 2^-8 for both; the float32 path keeps 2^-23 (D of its roundings are
+  in delta's term).
   F: rounding is relative only down to the smallest step.  The tensor-core decode keeps x =
   a_j * (V scale), relative to its largest, as 2^8 at most; E4M3's smallest step is 2^-9 and
   the second piece carries a factor of 32, so x is off by up to 2^-15, 2^-23 of the largest
-  (the prompt kernel keeps x as 1 or more at its largest, in f16, whose smallest half step is 2^-25),
+  (the prompt kernel keeps x in bf16, which has float32's smallest step),
   against each code: F = max_j(a_j * V scale) sum_j |V code|.  (A page's scale is at least its
   largest value / 448, so F matters only where the heaviest tokens' own values vanish.)
 """
@@ -354,6 +355,66 @@ def test_large_logits(hq, hkv, d, dt):
     want = orc.attend(f64(q), table, kv, [0, 70, 100])
     out = cache.attend(0, q.cuda(), i32(table), i32(kv), q_start=i32([0, 70, 100]), max_q_len=70)
     check_out(out, want, d, dt, dt == kvs.BF16)
+
+
+def stored(kv, k, v, d, hq, hkv, seed):
+    """A cache and its oracle that hold k and v (the requests' tokens one after the other) in shuffled pages."""
+    blocks = [-(-x // 16) for x in kv]
+    perm = np.random.default_rng(seed).permutation(sum(blocks))
+    table, at = np.full((len(kv), max(blocks)), -7), 0
+    for r, b in enumerate(blocks):
+        table[r, :b] = perm[at:at + b]
+        at += b
+    slots = np.concatenate([table[r, np.arange(x) // 16] * 16 + np.arange(x) % 16 for r, x in enumerate(kv)])
+    cache, orc = make(hq, hkv, d, sum(blocks), kvs.BF16), ref.Pages(sum(blocks), hkv, d)
+    cache.append(0, k.cuda(), v.cuda(), i32(slots))
+    orc.append(f64(k), f64(v), slots)
+    return cache, orc, table
+
+
+@pytest.mark.parametrize("new", [1, 2, 40, 150])
+@pytest.mark.parametrize("d", [64, 128])
+def test_logits_that_grow_by_far(d, new):
+    """Tokens in either half of a tile whose logits pass all before them by 2^60 to 2^300."""
+    g = torch.Generator().manual_seed(d + new)
+    kv, hq, hkv = [700, 330], 16, 2
+    rows = sum(kv)
+    sign = torch.sign(torch.randn((1, 1, d), generator=g))
+    size = torch.zeros((rows, 1, 1))
+    for j, a in ((3, 0.5), (70, 4), (100, 4.5), (130, 6), (200, 9), (450, 14), (700 + 90, 5), (700 + 180, 10)):
+        size[j] = a * (128 / d) ** 0.5
+    k = (size * sign + 0.25 * torch.randn((rows, hkv, d), generator=g)).to(torch.bfloat16)
+    v = torch.randn((rows, hkv, d), generator=g).to(torch.bfloat16)
+    gain = torch.tensor([1.0, 2.0, -1.0, 0.5, -2.0, 0.0, 1.5, 1.0] * 2).view(1, hq, 1)
+    q = (gain * sign + 0.1 * torch.randn((2 * new, hq, d), generator=g)).to(torch.bfloat16)
+    cache, orc, table = stored(kv, k, v, d, hq, hkv, d)
+    start = [0, new, 2 * new]
+    want = orc.attend(f64(q), table, kv, start)
+    out = cache.attend(0, q.cuda(), i32(table), i32(kv), q_start=i32(start), max_q_len=new)
+    check_out(out, want, d, kvs.BF16, True)
+    want = orc.attend(f64(q), table, kv, start, window=150)
+    out = cache.attend(0, q.cuda(), i32(table), i32(kv), q_start=i32(start), max_q_len=new, window=150)
+    check_out(out, want, d, kvs.BF16, True)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("zero", ["first", "last", "odd", "all"])
+def test_pages_of_zeros(zero, new):
+    """Pages whose values are all 0 have the smallest scale; their tokens keep their weights."""
+    g = torch.Generator().manual_seed(new)
+    kv, hq, hkv, d = [500, 140], 16, 2, 128
+    rows = sum(kv)
+    k = torch.randn((rows, hkv, d), generator=g).to(torch.bfloat16)
+    v = torch.randn((rows, hkv, d), generator=g)
+    pos = torch.cat([torch.arange(x) for x in kv])
+    gone = {"first": pos < 128, "last": pos >= 112, "odd": pos // 16 % 2 == 1, "all": pos >= 0}[zero]
+    v[gone] = 0
+    q = torch.randn((2 * new, hq, d), generator=g).to(torch.bfloat16)
+    cache, orc, table = stored(kv, k, v.to(torch.bfloat16), d, hq, hkv, 5)
+    start = [0, new, 2 * new]
+    want = orc.attend(f64(q), table, kv, start)
+    out = cache.attend(0, q.cuda(), i32(table), i32(kv), q_start=i32(start), max_q_len=new)
+    check_out(out, want, d, kvs.BF16, True)
 
 
 @pytest.mark.parametrize("dt", [kvs.BF16, kvs.F32])
