@@ -10,17 +10,17 @@
 // and o = O / l.  The scales are powers of two, so V's rides in x's exponent and V's codes
 // are exact in bf16.  x is rounded to 8 bits as the output is, and l sums the rounded x, so that a
 // row of one strong token has no error from it (with l of the exact x the whole error was up to
-// 1.43 times that of rounding the output alone, so 1.19; the exact l would be 4 % faster).  bf16 has
+// 1.43 times that of rounding the output alone, so 1.19, in the same time).  bf16 has
 // float32's exponents, so m need not follow the maximum: it moves, and O is rescaled, only where x would pass
-// 2^63 or l leave float32.  With x in f16, whose 2^16 strong tokens passed in every third half tile of
-// the 8192-token prompt, the exponentials taken again and O rescaled cost it 16 %.
+// 2^63 or l leave float32.  With x in f16, whose 2^16 strong tokens passed in four of ten tiles of
+// the 8192-token prompt, the exponentials taken again and O rescaled cost it a fifth.
 // Queries: exact down to 2^-10 of the row's largest element, an error of 2^-19 of the largest below that.
 //
 // How: work is cut as in the decode kernel: the 128-token tiles of all units laid end to
 // end and split evenly over one CTA per SM, partials of split units added by a join
 // kernel.  That also balances causal rows, whose units differ in length, and feeds all
 // SMs when rows are few and the context is long.  A unit's start counts as three tiles (with two
-// the CTA of the 8192-token prompt's shortest units ends last, 4 % later; four are 1 % slower).
+// the CTA of the 8192-token prompt's shortest units ends last, 12 % later; four are 1 % slower).
 // A split kernel first writes the queries' pieces in operand layout (a few percent of the
 // time; two warps of each CTA that did it took 15 to 27 thousand clocks a unit).
 // Per CTA: one warp copies K pages into a ring, one the queries, four convert V's codes to
@@ -32,14 +32,10 @@
 // first operand: from shared memory the two operands of both products, X's stores and V's
 // would be 368 KB a step, 2900 clocks at 128 bytes, against the tensor core's 2048.
 //
-// P is handed over in halves of 64 tokens: the first one's product runs under the second one's
-// exponentials, and the half that a thread holds fits its registers.
-//
-// Bound by the chain of one tile (two halves' exponentials, X's stores, the second half's product and the
-// next S), which only the other tile's overlaps: 3200 clocks a step of 128 tokens, against 2048 of matrix work,
-// 56 % of the tensor core's time.  Measured on 32/4 heads of 128: an 8192-token prompt 465 us
-// (1.18 PFLOP/s, 62 % of the measured bf16 rate), five chunks of 100 to 2048 tokens behind up to
-// 8192 333 us (1.13 PFLOP/s).
+// Bound by the chain of one tile (exponentials, X's store, its product and the next S), which only
+// the other tile's overlaps: 2950 clocks a step of 128 tokens, against 2048 of matrix work, 61 % of the
+// tensor core's time.  Measured on 32/4 heads of 128: an 8192-token prompt 437 us (1.26 PFLOP/s,
+// 66 % of the measured bf16 rate), five chunks of 100 to 2048 tokens behind up to 8192 314 us (1.20 PFLOP/s).
 #include "paged_mma.cuh"
 
 namespace kvs {
@@ -58,10 +54,10 @@ constexpr int kSetup = 3;                // what a unit's start costs, in tiles,
 constexpr int kRows = 128;               // rows of a tile of queries
 constexpr int kChunk = 512;              // requests of one round of the search
 constexpr float kLog2e = 1.4426950408889634f;
-// A row's reference moves where x would pass 2^kFarX or a part of l 2^kFarL.  What passes kLimit shows it: half a
-// tile's part of l, and a block's sum of x times kSumShare.  Sums of 2^26 tokens then stay within float32.
+// A row's reference moves where x would pass 2^kFarX or a part of l 2^kFarL.  What passes kLimit shows it: a tile's
+// part of l, and a block's sum of x times kSumShare.  Sums of 2^26 tokens then stay within float32.
 constexpr float kFarX = 63.f, kFarL = 99.f;
-constexpr float kLimit = 0x1p106f, kSumShare = 0x1p38f;
+constexpr float kLimit = 0x1p107f, kSumShare = 0x1p39f;
 
 // Units of request r: groups of `per` query tokens, all KV heads alike.
 struct Req {
@@ -243,7 +239,7 @@ struct Walk {
 
 struct Misc {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], drain;
-  uint64_t s_ready[2], p_ready[2][2], half_done[2], o_done[2];
+  uint64_t s_ready[2], p_ready[2], o_done[2];
   uint64_t q_ready[kSlots], q_empty[kQStages], sc_ready[kSlots];
   uint32_t tmem;
   alignas(16) float ks[kSlots][kTileBlocks], vs[kSlots][kTileBlocks];
@@ -264,12 +260,11 @@ struct Cfg {
   static_assert(SMEM + (int)sizeof(Search) <= 227 * 1024, "shared memory");
 };
 
-// The scales of half a tile, 64 tokens, in registers: the operands' traffic starves shared-memory loads.
-constexpr int kHalf = kTile / 2, kHalfBlocks = kTileBlocks / 2;
 __device__ __forceinline__ float scale_log2(float s) { return (float)((__float_as_int(s) >> 23) - 127); }
 __device__ __forceinline__ float scale_inverse(float s) { return __int_as_float((254 << 23) - __float_as_int(s)); }
-struct Half {
-  float ks[kHalfBlocks], vs[kHalfBlocks];
+// The scales of a tile in registers: the operands' traffic starves shared-memory loads.
+struct Scales {
+  float ks[kTileBlocks], vs[kTileBlocks];
   __device__ __forceinline__ float ev(int b) const { return scale_log2(vs[b]); }
   __device__ __forceinline__ float iv(int b) const { return scale_inverse(vs[b]); }
 };
@@ -280,20 +275,18 @@ __device__ __forceinline__ void add_bf16x2(float& lo, float& hi, uint32_t v) {
       : "+f"(lo), "+f"(hi) : "r"(v));
 }
 
-// x = 2^(t - ref) of the row's half of a tile, as bf16 pairs; the largest sum of a block to `most`.
+// x = 2^(t - ref) of the row's tokens of a tile, as bf16 pairs; the largest sum of a block to `most`.
 // Returns the row's part of l.
-__device__ __forceinline__ float row_exp(uint32_t t_s, const Half& y, float c, float ref, uint32_t (&h)[32], float& most) {
+__device__ __forceinline__ float row_exp(uint32_t t_s, const Scales& y, float c, float ref, uint32_t (&h)[64], float& most) {
   float l = 0.f;
   most = 0.f;
-  uint32_t r[2][32];
-  ld32_start(t_s, r[0]);
+  uint32_t r[2][16];
+  ld16_start(t_s, r[0]);
 #pragma unroll
-  for (int b = 0; b < kHalfBlocks; ++b) {
-    uint32_t* v = r[b / 2 & 1] + b % 2 * 16;
-    if (b % 2 == 0) {
-      ld32_wait(r[b / 2 & 1]);
-      if (b + 2 < kHalfBlocks) ld32_start(t_s + 16 * (b + 2), r[(b / 2 + 1) & 1]);
-    }
+  for (int b = 0; b < kTileBlocks; ++b) {
+    ld16_wait(r[b & 1]);
+    if (b + 1 < kTileBlocks) ld16_start(t_s + 16 * (b + 1), r[(b + 1) & 1]);
+    uint32_t* v = r[b & 1];
     const float m1 = y.ks[b] * c, s1 = y.ev(b) - ref;
     const uint64_t mul = pack2(m1, m1), sub = pack2(s1, s1);
     float sum0 = 0.f, sum1 = 0.f;
@@ -318,26 +311,26 @@ __device__ __forceinline__ uint32_t seen_of(int pos, int lo, int hi) {
   return (1u << up) - (1u << min(up, down));
 }
 
-// Half a tile in general: rows that do not see all of it, that have seen nothing yet, or whose x is out of range.
-// Looks at the maxima first and moves a reference where it has to.  Writes x to TMEM over the half's S.  A loop, apart
-// from row_exp: few halves come here, and one loop with both forms cost the others 13 % in registers and moves.
+// A tile in general: rows that do not see all of it, that have seen nothing yet, or whose x is out of range.
+// Looks at the maxima first and moves a reference where it has to.  Writes x to TMEM over S, whose columns it has read
+// by then.  A loop, apart from row_exp: few tiles come here, and one loop with both forms cost the others 13 % in
+// registers and moves.
 struct Row {
   float m, f, add;
 };
-__device__ __forceinline__ void half_general(Row& w, uint32_t t_h, uint32_t t_p, const float* ks, const float* vs, float c,
-                                             int pos, int lo, int hi, uint32_t gone) {
+__device__ __forceinline__ void tile_general(Row& w, uint32_t t_s, const float* ks, const float* vs, float c, int pos,
+                                             int lo, int hi, uint32_t gone) {
   float top = -INFINITY, top_l = -INFINITY;  // of x's and of l's logarithms
 #pragma unroll 1
-  for (int b = 0; b < kHalfBlocks; b += 2) {
-    uint32_t s[32];
-    ld32_start(t_h + 16 * b, s);
-    ld32_wait(s);
+  for (int b = 0; b < kTileBlocks; b += 2) {
+    float s[32];
+    umma::ld32(t_s + 16 * b, s);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint32_t seen = gone >> (b + e) & 1 ? 0u : seen_of(pos + 16 * (b + e), lo, hi);
       float v = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v = fmaxf(v, seen >> k & 1 ? __uint_as_float(s[16 * e + k]) : -INFINITY);
+      for (int k = 0; k < 16; ++k) v = fmaxf(v, seen >> k & 1 ? s[16 * e + k] : -INFINITY);
       if (v > -INFINITY) {
         top = fmaxf(top, fmaf(v, ks[b + e] * c, scale_log2(vs[b + e])));
         top_l = fmaxf(top_l, v * (ks[b + e] * c));
@@ -352,10 +345,10 @@ __device__ __forceinline__ void half_general(Row& w, uint32_t t_h, uint32_t t_p,
   const float ref = w.m == -INFINITY ? 0.f : w.m;
   w.add = 0.f;
 #pragma unroll 1
-  for (int b = 0; b < kHalfBlocks; b += 2) {
-    uint32_t s[32], h[16];
-    ld32_start(t_h + 16 * b, s);
-    ld32_wait(s);
+  for (int b = 0; b < kTileBlocks; b += 2) {
+    float s[32];
+    uint32_t h[16];
+    umma::ld32(t_s + 16 * b, s);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint32_t seen = gone >> (b + e) & 1 ? 0u : seen_of(pos + 16 * (b + e), lo, hi);
@@ -364,7 +357,7 @@ __device__ __forceinline__ void half_general(Row& w, uint32_t t_h, uint32_t t_p,
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int i = 16 * e + 2 * k;
-        float x0 = ex2(fmaf(__uint_as_float(s[i]), m1, s1)), x1 = ex2(fmaf(__uint_as_float(s[i + 1]), m1, s1));
+        float x0 = ex2(fmaf(s[i], m1, s1)), x1 = ex2(fmaf(s[i + 1], m1, s1));
         if (!(seen >> (2 * k) & 1)) x0 = 0.f;
         if (!(seen >> (2 * k + 1) & 1)) x1 = 0.f;
         const __nv_bfloat162 p = __floats2bfloat162_rn(x0, x1);
@@ -373,8 +366,8 @@ __device__ __forceinline__ void half_general(Row& w, uint32_t t_h, uint32_t t_p,
       }
       w.add = fmaf(sum, scale_inverse(vs[b + e]), w.add);
     }
-    st16(t_p + 8 * b, reinterpret_cast<const float*>(h));
-    wait_st();                               // the second half's S is read after the first's x is written
+    st16(t_s + 8 * b, reinterpret_cast<const float*>(h));
+    wait_st();                               // before the next load
   }
 }
 
@@ -480,9 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
     mbar_init(smem_u32(&ms.drain), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms.s_ready[i]), 1);
-      mbar_init(smem_u32(&ms.p_ready[i][0]), 4);
-      mbar_init(smem_u32(&ms.p_ready[i][1]), 4);
-      mbar_init(smem_u32(&ms.half_done[i]), 1);
+      mbar_init(smem_u32(&ms.p_ready[i]), 4);
       mbar_init(smem_u32(&ms.o_done[i]), 1);
       mbar_init(smem_u32(&ms.q_empty[i]), 1);
     }
@@ -667,26 +658,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
                  id_qk, k > 0);
       commit(on, smem_u32(&ms.s_ready[x]));
     };
-    auto pv = [&](int x, int n, int half, bool fresh) {   // O of tile x with half of V number n
+    auto products = [&](int x, int n, uint32_t parity, bool first, bool last) {    // O, and the next S, of tile x
+      ok = ok && warp_wait(smem_u32(&ms.p_ready[x]), parity);
+      if (!ok) return;
+      umma::fence_after();
       const uint32_t bv = desc_lo(smem_u32(sv + (n % kVStages) * C::V), D * 16);
 #pragma unroll
-      for (int k = 0; k < kHalf / 16; ++k)
-        mma_f16_ts(on, tmem + 256 + x * 128, tmem + x * 128 + half * (kHalf / 2) + k * 8,
-                   bv + (half * (kHalf / 16) + k) * (2 * D), desc_hi(128), id_pv, !(fresh && k == 0));
-    };
-    // a tile's products as the halves of its P come
-    auto products = [&](int x, int n, uint32_t parity, bool first, bool last) {
-      ok = ok && warp_wait(smem_u32(&ms.p_ready[x][0]), parity);
-      if (!ok) return;
-      umma::fence_after();
-      pv(x, n, 0, first);
-      commit(on, smem_u32(&ms.half_done[x]));
-      ok = warp_wait(smem_u32(&ms.p_ready[x][1]), parity);
-      if (!ok) return;
-      umma::fence_after();
-      pv(x, n, 1, false);                                 // before the next S, which overwrites P
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_f16_ts(on, tmem + 256 + x * 128, tmem + x * 128 + k * 8, bv + k * (2 * D), desc_hi(128), id_pv,
+                   !(first && k == 0));
       if (last) commit(on, smem_u32(&ms.o_done[x]));
-      else qk(x, n + 1);
+      else qk(x, n + 1);                                  // behind the product, whose P it overwrites
     };
     while (w.nt > 0 && ok) {
       const bool two = w.u.cnt > qpt;
@@ -761,57 +743,50 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
         if (t > 0) ok = ok && warp_wait(smem_u32(&ms.s_ready[x]), count & 1);
         if (!ok) break;
         umma::fence_after();
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const int from = base + half * kHalf;
-          const uint32_t gone = bad >> (half * kHalfBlocks) & ((1u << kHalfBlocks) - 1);
-          const uint32_t t_h = t_s + half * kHalf, t_p = t_s + half * (kHalf / 2);      // P: two tokens to a column
-          // Mostly all rows see all of the half and the reference serves, so the exponentials are taken at once.  The
-          // first reference is any token's t: bf16 has float32's range.
-          bool general = from < all_lo || from + kHalf > all_hi || gone;
-          if (t + half == 0 && !general) m = fmaf(ld1(t_h), ms.ks[slot][0] * c, scale_log2(ms.vs[slot][0]));
-          general = general || __any_sync(0xffffffffu, !(fabsf(m) < 1e30f));
-          float f = 1.f, add;
+        // Mostly all rows see all of the tile and the reference serves, so the exponentials are taken at once.  The
+        // first reference is any token's t: bf16 has float32's range.
+        bool general = base < all_lo || base + kTile > all_hi || bad;
+        if (t == 0 && !general) m = fmaf(ld1(t_s), ms.ks[slot][0] * c, scale_log2(ms.vs[slot][0]));
+        general = general || __any_sync(0xffffffffu, !(fabsf(m) < 1e30f));
+        float f = 1.f, add;
+        if (!general) {
+          Scales y;
+          *reinterpret_cast<float4*>(y.ks) = *reinterpret_cast<const float4*>(ms.ks[slot]);
+          *reinterpret_cast<float4*>(y.ks + 4) = *reinterpret_cast<const float4*>(ms.ks[slot] + 4);
+          *reinterpret_cast<float4*>(y.vs) = *reinterpret_cast<const float4*>(ms.vs[slot]);
+          *reinterpret_cast<float4*>(y.vs + 4) = *reinterpret_cast<const float4*>(ms.vs[slot] + 4);
+          uint32_t h[64];
+          float most;
+          add = row_exp(t_s, y, c, m, h, most);
+          general = __any_sync(0xffffffffu, !(fmaxf(most * kSumShare, add) <= kLimit));
           if (!general) {
-            Half y;
-            *reinterpret_cast<float4*>(y.ks) = *reinterpret_cast<const float4*>(ms.ks[slot] + half * kHalfBlocks);
-            *reinterpret_cast<float4*>(y.vs) = *reinterpret_cast<const float4*>(ms.vs[slot] + half * kHalfBlocks);
-            uint32_t h[32];
-            float most;
-            add = row_exp(t_h, y, c, m, h, most);
-            general = __any_sync(0xffffffffu, !(fmaxf(most * kSumShare, add) <= kLimit));
-            if (!general) st32(t_p, h);
+            st32(t_s, h);                                   // P over S, two tokens to a column
+            st32(t_s + 32, h + 32);
           }
-          if (general) {
-            Row r{m};
-            half_general(r, t_h, t_p, ms.ks[slot] + half * kHalfBlocks, ms.vs[slot] + half * kHalfBlocks, c, from, lo, hi,
-                         gone);
-            m = r.m;
-            f = r.f;
-            add = r.add;
-          }
-          l = fmaf(l, f, add);
-          // S was issued behind the previous tile's product, so that is done with O; the first half's may not be
-          if (t + half > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-            if (half) {
-              ok = warp_wait(smem_u32(&ms.half_done[x]), count & 1);
-              if (!ok) break;
-              umma::fence_after();
-            }
-#pragma unroll
-            for (int j = 0; j < D; j += 16) {
-              float o[16];
-              ld16(t_o + j, o);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= f;
-              st16(t_o + j, o);
-            }
-          }
-          wait_st();
-          umma::fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready[x][half]));
         }
+        if (general) {
+          Row r{m};
+          tile_general(r, t_s, ms.ks[slot], ms.vs[slot], c, base, lo, hi, bad);
+          m = r.m;
+          f = r.f;
+          add = r.add;
+        }
+        l = fmaf(l, f, add);
+        // S was issued behind the previous product, so that is done with O
+        if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+          for (int j = 0; j < D; j += 16) {
+            float o[16];
+            ld16(t_o + j, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] *= f;
+            st16(t_o + j, o);
+          }
+        }
+        wait_st();
+        umma::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready[x]));
       }
       if (!ok) break;
       advance(walks[(seg + 1) & 1], w, true);
