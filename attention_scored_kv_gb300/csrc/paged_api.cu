@@ -121,8 +121,8 @@ PagedAttendPlan plan_attend(const kvs_paged* pc, int n_reqs, int stride, int tot
   const PagedDev& d = pc->dev;
   size_t recs = 0;
   // The decode kernel's cost grows with its query rows, the prompt kernel's does not until 128.  32/4 heads of
-  // 128, decode against prompt: 16 rows 29 against 40 us (16 x 4096 tokens) and 22 against 39 (1 x 32768); 32 rows
-  // 57 against 43, 253 against 204 (16 x 32768) and 87 against 49 (64 x 1000).  Block masses are the decode kernel's.
+  // 128, decode against prompt: 16 rows 29 against 39 us (16 x 4096 tokens) and 24 against 33 (1 x 32768); 32 rows
+  // 57 against 39, 253 against 177 (16 x 32768) and 87 against 46 (64 x 1000).  Block masses are the decode kernel's.
   const long long need = (long long)max_q_len * d.G;       // query rows of a unit
   p.splits = 1;
   if (pc->tensor && (need <= 16 || (mass && need <= 32))) {
