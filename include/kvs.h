@@ -621,7 +621,10 @@ KVS_API kvs_status kvs_paged_gather(kvs_paged* pc, int32_t layer, int32_t n_rows
  * d_scratch: device memory of kvs_paged_attend_scratch_bytes(), 256-byte aligned, whose
  * contents before and after mean nothing; calls that may overlap need scratch of their
  * own.  With bf16 in_dtype probabilities are rounded to 8 significant bits or more before
- * their product with V; sums and softmax statistics are float32. */
+ * their product with V; sums and softmax statistics are float32.  On the tensor cores V's
+ * scale rides in the probability's exponent: where a page's V scale is 2^-100 of that of a
+ * row's heaviest token (a page of zeros, 2^-100, beside values of 224 to 448), weights under
+ * 2^-26 of the heaviest are taken as 0, and a bit sooner for every factor of 2 more. */
 KVS_API size_t kvs_paged_attend_scratch_bytes(const kvs_paged* pc, int32_t n_reqs, int32_t table_stride,
                                               int32_t total_q, int32_t max_q_len, int32_t block_mass);
 KVS_API kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const int32_t* d_block_table,
