@@ -101,6 +101,16 @@ __device__ __forceinline__ uint32_t float2_to_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The same in E5M2, whose codes are the upper bytes of f16.
+__device__ __forceinline__ uint32_t float2_to_e5m2x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 e5m2x2_to_float2(uint32_t codes16) {
+  const uint32_t h = __byte_perm(codes16, 0, 0x1404);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
 
 // Request of packed row t: the last r with row_start[r] <= t.
 __device__ __forceinline__ int request_of(const int32_t* row_start, int n, int t) {

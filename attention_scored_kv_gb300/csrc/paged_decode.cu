@@ -4,27 +4,32 @@
 // For a unit (request, KV head) with R query rows (tokens x heads of the group) and a
 // tile of 128 cached tokens j:
 //   S^T = K Q^T        [128 tokens x rows]   E4M3 x E4M3 matrix instructions
-//   t_jr = S_jr kscale_j c_r + log2 vscale_j,  m_r = running maximum of t - 8
-//   x_jr = 2^(t_jr - m_r),  l_r += x_jr / vscale_j
-//   O^T += V^T X       [D x rows]
+//   t_jr = S_jr kscale_j c_r + log2 vscale_j,  top_r = the tile's maximum of t
+//   x_jr = 2^(t_jr - top_r + 15),  P^T = V^T X   [D x rows]   E4M3 x E5M2
+//   M_r = running maximum of top, w_r = 2^(top_r - M_r - 15)
+//   l_r += w_r sum_j x_jr / vscale_j,  O_r += w_r P_r    (both moved when M moves)
 // and o_r = O_r / l_r.  x carries V's scale in its exponent (the scales are powers of two),
-// so x <= 256 whatever the scales are, and K and V enter the tensor core as they are stored.
+// so x <= 2^15 whatever the scales are, and K and V enter the tensor core as they are stored.
 //
 // Precision: E4M3 holds 4 significant bits.  A bf16 query (8 bits) is split in two pieces
 // of 4, hi = rn(q), lo = rn(16 (q - hi)) after a power of two brings the row's largest to
-// (224, 448]: exact for elements within 2^14 of it.  A probability is split the same way:
-// its 8 bits are off by at most 2^-9 of it, half of what rounding the output to bf16 may
-// be.  The pieces are
-// separate columns of the same instruction, N = 2 rows, so 8 rows fill its smallest N of
-// 16 and the split is free there.  Accumulation is float32.
+// (224, 448]: exact for elements within 2^14 of it, off by 2^-22 of it at most below.  A
+// probability is three E5M2 pieces, each of 8 times the remainder of the one before: off by
+// at most 2^-11 of itself down to 2^-29 of the tile's heaviest and by 2^-38 of the heaviest
+// below that.  The range is what matters: a head whose sink takes nearly all the weight has a
+// value near 0 there, and its output is the sum of very many small weights.  Two E4M3
+// pieces against the row's maximum lost a quarter of such an output at 131072 tokens.  For the same reason
+// every tile has its own reference, and its product is added in registers.  The pieces are
+// separate columns of the same instructions; accumulation is float32.
 //
 // How: the 128-token tiles of all units are laid end to end and cut evenly over a
 // persistent grid, two CTAs to an SM (each CTA finds its range from the device lengths by
 // itself); a unit that a cut splits leaves float32 partials which the join kernel adds.
 // Per CTA one warp issues the pages' bulk copies into a ring, one the matrix instructions,
 // four warps the softmax (a thread is a token, so scales and masks are one per thread and
-// the probabilities go to shared memory as bytes).  S is double buffered: the next tile's S
-// is computed under this one's softmax.
+// the probabilities go to shared memory as bytes; the thread of token i also sums dimension i of the
+// products).  S is double buffered: the next tile's S is computed under this one's softmax.  So is the
+// product up to 16 rows: the last one is added while the next is computed.
 //
 // Bound by the pages' bytes.  Measured on 32/4 heads of 128: 16 contexts of 32768 tokens
 // 89 us (5.95 TB/s, 89 % of the measured copy rate), 64 of 1024 to 32768 with masses 187 us;
@@ -42,10 +47,10 @@ constexpr int kTileBlocks = kTile / kBlock;
 constexpr int kThreads = 192;            // 4 softmax warps, copies, matrix instructions
 constexpr int kCtasPerSm = 2;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTop = 8.f;              // the largest x is 2^8
-// Scales of the second pieces: the largest that keep them in range.  A query's first piece
-// is at most 448, where half a step is 16; a probability's 256, with half a step of 8 below it.
-constexpr float kLoQ = 16.f, kLoP = 32.f;
+constexpr float kTop = 15.f;             // the largest x is 2^15, E5M2's largest power of two
+// Factor of a query's second piece, the largest that keeps it in range: the first is at most 448, where half
+// a step is 16.  Of a probability's second and third against the one before: half a step of 3 bits.
+constexpr float kLoQ = 16.f, kLoP = 8.f;
 
 // Tiles of request r's units (all KV heads alike) and their ranges.
 struct Unit {
@@ -117,43 +122,54 @@ __device__ long long total_tiles(const PagedAttend& a, long long* s_sum) {
 
 template <int D, int RT>
 struct Cfg {
-  static constexpr int N = 2 * RT;                       // columns: both pieces of the rows
+  static constexpr int N = 2 * RT;                       // columns of S: both pieces of the queries
+  static constexpr int NP = RT == 8 ? 32 : 3 * RT;       // of the product: three of the probabilities (a multiple of 16)
+  static constexpr int NO = RT == 32 ? 1 : 2;            // products in TMEM
   static constexpr int PAGE = 16 * D;                    // bytes of a page of K or V of one head
   static constexpr int HALF = kTileBlocks * PAGE;        // K (or V) of a stage
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int Q = N * D, P = N * kTile;
-  static constexpr int MISC = 4096;
-  static constexpr int ROOM = 227 * 1024 / kCtasPerSm - 1024 - 2 * Q - P - MISC;
+  static constexpr int Q = N * D, P = NP * kTile;
+  static constexpr int MISC = RT == 32 ? 5120 : 4096;
+  static constexpr int ROOM = 227 * 1024 / kCtasPerSm - 1024 - Q - P - MISC;
   static constexpr int NS = ROOM / STAGE < 6 ? ROOM / STAGE : 6;
   // an M of 128 reads a further 1 KB behind the last page of V for D = 64: Q is there
-  static constexpr int SMEM = NS * STAGE + 2 * Q + P + MISC + 1024;
-  static constexpr int TMEM = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 256;
-  static_assert(NS >= 2 && 3 * N <= TMEM && (SMEM + 1024) * kCtasPerSm <= 228 * 1024, "ring, TMEM, shared memory");
+  static constexpr int SMEM = NS * STAGE + Q + P + MISC + 1024;
+  static constexpr int COLS = 2 * N + NO * NP, TMEM = COLS <= 128 ? 128 : 256;
+  static_assert(NS >= 2 && COLS <= TMEM && TMEM * kCtasPerSm <= 512 && (SMEM + 1024) * kCtasPerSm <= 228 * 1024,
+                "ring, TMEM, shared memory");
 };
 
+// What a tile does to a row: x is 2^(t - ref); the sums so far are multiplied by `keep`, the tile's part of l by
+// `weight`; the product before it by `last`, that is its own weight times `keep`.
+struct RowStep {
+  float ref, keep, weight, last;
+};
+
+template <int RT>
 struct Misc {
   uint64_t full[6], empty[6], s_ready[2], p_ready, o_done, q_ready, drain;
   uint32_t tmem;
-  int token[32];         // query token of a row
+  int token[RT];         // query token of a row
   int start_r, start_h, start_t;
   long long sums[kThreads / 32];
   float ks[6][kTileBlocks], ev[6][kTileBlocks], iv[6][kTileBlocks];   // of each stage's blocks
-  float qc[2][32];
-  float wmax[2][4][32];
-  float wsum[4][32];
+  float qc[2][RT];
+  float wmax[2][4][RT];
+  float wsum[4][RT];
+  alignas(16) RowStep step[4][RT];       // of each softmax warp, alike
 };
-static_assert(sizeof(Misc) <= 4096, "Misc");
 
 template <int D, int RT, bool MASS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const PagedAttend a) {
   using C = Cfg<D, RT>;
-  constexpr int N = C::N;
+  constexpr int N = C::N, NP = C::NP;
+  static_assert(sizeof(Misc<RT>) <= C::MISC, "Misc");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = smem;
   uint8_t* sq = ring + C::NS * C::STAGE;
-  uint8_t* sp = sq + 2 * C::Q;
-  Misc& ms = *reinterpret_cast<Misc*>(sp + C::P);
+  uint8_t* sp = sq + C::Q;
+  Misc<RT>& ms = *reinterpret_cast<Misc<RT>*>(sp + C::P);
   const PagedDev& d = a.d;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
@@ -300,25 +316,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
     for (int i = max(0, count - C::NS); i < count; ++i) mbar_wait(smem_u32(&ms.full[i % C::NS]), (i / C::NS) & 1);
   } else if (warp == 5) {
     // ---- matrix instructions
-    constexpr uint32_t id = idesc_e4m3(128, N);
+    constexpr uint32_t id_qk = idesc_f8(128, N), id_pv = idesc_f8(128, NP, kE4M3, kE5M2);
     const uint32_t on = elect();
     int count = 0, seg = 0;
     bool ok = true;
-    auto pv = [&](int i, int nb, bool fresh) {              // tile number i of the CTA
+    auto pv = [&](int i, int nb) {                          // tile number i of the CTA
       const int st = i % C::NS, steps = (nb + 1) / 2;
       umma::fence_after();
-      const uint32_t av = desc_lo(smem_u32(ring + st * C::STAGE + C::HALF), C::PAGE), bp = desc_lo(smem_u32(sp), N * 16);
+      const uint32_t av = desc_lo(smem_u32(ring + st * C::STAGE + C::HALF), C::PAGE), bp = desc_lo(smem_u32(sp), NP * 16);
 #pragma unroll
       for (int k = 0; k < kTileBlocks / 2; ++k)
         if (k < steps)
-          mma_e4m3(on, t_o, av + k * (2 * C::PAGE / 16), desc_hi(128), bp + k * (2 * N), desc_hi(128), id,
-                   !(fresh && k == 0));
+          mma_f8(on, t_o + (i % C::NO) * NP, av + k * (2 * C::PAGE / 16), desc_hi(128), bp + k * (2 * NP), desc_hi(128),
+                 id_pv, k > 0);
       commit(on, smem_u32(&ms.empty[st]));
       commit(on, smem_u32(&ms.o_done));
     };
     while (w.left > 0 && ok) {
       ok = warp_wait(smem_u32(&ms.q_ready), seg & 1);
-      const uint32_t bq = desc_lo(smem_u32(sq + (seg & 1) * C::Q), 128);
+      const uint32_t bq = desc_lo(smem_u32(sq), 128);
       int nb_before = 0;
       for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
         const int st = count % C::NS, nb = max(0, min(kTileBlocks, w.u.nb - t * kTileBlocks));
@@ -328,18 +344,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
         const uint32_t ak = desc_lo(smem_u32(ring + st * C::STAGE), 128);
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
-          mma_e4m3(on, tmem + (count & 1) * N, ak + k * 16, desc_hi(8 * D), bq + k * 16, desc_hi(8 * D), id, k > 0);
+          mma_f8(on, tmem + (count & 1) * N, ak + k * 16, desc_hi(8 * D), bq + k * 16, desc_hi(8 * D), id_qk, k > 0);
         commit(on, smem_u32(&ms.s_ready[count & 1]));
         if (t > w.t0) {
           ok = warp_wait(smem_u32(&ms.p_ready), (count - 1) & 1);
           if (!ok) break;
-          pv(count - 1, nb_before, t - 1 == w.t0);
+          pv(count - 1, nb_before);
         }
         nb_before = nb;
       }
       if (ok) ok = warp_wait(smem_u32(&ms.p_ready), (count - 1) & 1);
       if (!ok) break;
-      pv(count - 1, nb_before, w.nt == 1);
+      pv(count - 1, nb_before);
       ++seg;
       w.next(a);
     }
@@ -377,7 +393,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
       for (int o = TPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const int e = scale_exp(amax);
       const float up = exp2_int(-e);
-      uint8_t* base = sq + buf * C::Q;
 #pragma unroll
       for (int i = 0; i < E; i += 4) {
         uint32_t hi[2], lo[2];
@@ -389,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
           lo[u] = float2_to_e4m3x2((f - back.x) * kLoQ, (g - back.y) * kLoQ);
         }
         const int dim = part * E + i;
-        *reinterpret_cast<uint32_t*>(base + k_code(D, row, dim)) = hi[0] | hi[1] << 16;
-        *reinterpret_cast<uint32_t*>(base + k_code(D, row + RT, dim)) = lo[0] | lo[1] << 16;
+        *reinterpret_cast<uint32_t*>(sq + k_code(D, row, dim)) = hi[0] | hi[1] << 16;
+        *reinterpret_cast<uint32_t*>(sq + k_code(D, row + RT, dim)) = lo[0] | lo[1] << 16;
       }
       if (part == 0) ms.qc[buf][row] = !live ? 0.f : amax <= kFloatMax ? exp2_int(e) * qk : NAN;
       umma::fence_async_smem();
@@ -411,16 +426,46 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
     int count = 0, seg = 0;
     bool ok = true;
     while (w.left > 0 && ok) {
-      float m[RT], l[RT];
+      float l[RT], o[RT];                                  // of the thread's token and of its dimension
 #pragma unroll
-      for (int r = 0; r < RT; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
+      for (int r = 0; r < RT; ++r) l[r] = o[r] = 0.f;
+      // lane r has row r's maximum so far and the weight of the last tile's product
+      float most = -INFINITY, weight = 0.f;
       const float* qc = ms.qc[seg & 1];
+      RowStep* step = ms.step[warp];
       const int rows = w.u.n * d.G;
-      for (int t = w.t0; t < w.t0 + w.nt && ok; ++t, ++count) {
+      // adds the product of tile number i; `keep` and `part` of a step: the sums so far and the product times these
+      auto add_product = [&](int i, auto keep, auto part) {
+        const uint32_t to = t_o + (i % C::NO) * NP + lanes;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) o[r] *= keep(step[r]);
+        if constexpr (RT == 8) {
+          float s[32];
+          umma::ld32(to, s);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            o[r] = fmaf(fmaf(fmaf(s[r + 2 * RT], 1.f / kLoP, s[r + RT]), 1.f / kLoP, s[r]), part(step[r]), o[r]);
+        } else {
+#pragma unroll
+          for (int r0 = 0; r0 < RT; r0 += 16) {
+            float s[3][16];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) ld16(to + i * RT + r0, s[i]);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              o[r0 + r] = fmaf(fmaf(fmaf(s[2][r], 1.f / kLoP, s[1][r]), 1.f / kLoP, s[0][r]), part(step[r0 + r]), o[r0 + r]);
+          }
+        }
+      };
+      auto add_last = [&](int t) {
+        if (t > w.t0)
+          add_product(count - 1, [](const RowStep& y) { return y.keep; }, [](const RowStep& y) { return y.last; });
+      };
+      for (int t = w.t0; t < w.t0 + w.nt; ++t, ++count) {
         const int st = count % C::NS;
-        ok = mbar_wait(smem_u32(&ms.s_ready[count & 1]), (count >> 1) & 1);
+        ok = ok && mbar_wait(smem_u32(&ms.s_ready[count & 1]), (count >> 1) & 1);
         // the scales came with the stage: its barrier has completed, this orders the reads
-        if (ok) ok = mbar_wait(smem_u32(&ms.full[st]), (count / C::NS) & 1);
+        ok = ok && mbar_wait(smem_u32(&ms.full[st]), (count / C::NS) & 1);
         umma::fence_after();
         const int blk = tid >> 4, b = w.u.b0 + t * kTileBlocks;
         const float ks = ms.ks[st][blk], ev = ms.ev[st][blk], iv = ms.iv[st][blk];
@@ -454,67 +499,76 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
           if (lane == (r & 31)) ms.wmax[count & 1][warp][r] = top;
         }
         named_sync(1, 128);
-        bool grew = false;
-        float f[RT];
+        if (!ok) break;
+        if (lane < RT) {
+          const auto& wm = ms.wmax[count & 1];
+          const float top = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
+          const float now = fmaxf(most, top);
+          RowStep y;
+          y.ref = top > -INFINITY ? top - kTop : 0.f;      // hidden: 2^-inf; a NaN stays one
+          y.keep = now > -INFINITY ? ex2(most - now) : 1.f;
+          y.last = weight * y.keep;
+          y.weight = weight = top > -INFINITY ? ex2(top - now) * 0x1p-15f : 0.f;
+          most = now;
+          step[lane] = y;
+        }
+        __syncwarp();
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          const float top = fmaxf(fmaxf(ms.wmax[count & 1][0][r], ms.wmax[count & 1][1][r]),
-                                  fmaxf(ms.wmax[count & 1][2][r], ms.wmax[count & 1][3][r])) - kTop;
-          const float now = fmaxf(m[r], top);
-          f[r] = 1.f;
-          if (now > m[r]) {
-            f[r] = ex2(m[r] - now);
-            grew = true;
-          }
-          m[r] = now;
-          x[r] = ex2(x[r] - (now > -INFINITY ? now : 0.f));       // hidden: 2^-inf; a NaN stays one
-          l[r] = fmaf(l[r], f[r], x[r] * iv);
+          const RowStep y = step[r];
+          x[r] = ex2(x[r] - y.ref);
+          l[r] = fmaf(l[r], y.keep, x[r] * iv * y.weight);
         }
         if (MASS) {
-          // the blocks' sums, as log2, for the rows of one token
-          float keep = 0.f, ref = 0.f;
+          // The blocks' sums, as log2, for the rows of one token.  Each exchange halves the rows of a lane and
+          // doubles the tokens that they are summed over, so that 16 lanes sum RT rows in RT shuffles, not 4 RT.
+          float y[RT];
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            float s = x[r] * iv;
+          for (int r = 0; r < RT; ++r) y[r] = x[r] * iv;
+          int row = 0;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if ((lane & 15) == (r & 15)) { keep = s; ref = m[r]; }
-            if ((r & 15) == 15 || r == RT - 1) {
-              const int row = (r & ~15) + (lane & 15);
-              if (row <= r && row < rows && b + blk < w.u.b0 + w.u.nb)
-                a.blk[((size_t)w.r * a.table_stride + b + blk) * d.Hq + w.h * d.G + row] = __log2f(keep) + ref;
+          for (int o = 8, n = RT / 2; o > 0; o >>= 1, n >>= 1) {
+            if (n > 0) {
+              const bool up = lane & o;
+              row = 2 * row + up;
+#pragma unroll
+              for (int r = 0; r < n; ++r)
+                y[r] = (up ? y[r + n] : y[r]) + __shfl_xor_sync(0xffffffffu, up ? y[r] : y[r + n], o);
+            } else {
+              y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
             }
           }
-        }
-        // the previous product is done with the probabilities' buffer and the output
-        if (ok && count > 0) ok = mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
-        umma::fence_after();
-        if (grew && t > w.t0) {                            // the same in all threads
+          constexpr int EACH = RT < 16 ? 1 : RT / 16;      // rows of a lane, neighbours; of RT = 8 two lanes have one
 #pragma unroll
-          for (int c = 0; c < N; c += 16) {
-            float o[16];
-            ld16(t_o + lanes + c, o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= f[(c + i) % RT];
-            st16(t_o + lanes + c, o);
+          for (int i = 0; i < EACH; ++i) {
+            const int r = row * EACH + i;
+            if ((RT >= 16 || !(lane & 1)) && r < rows && b + blk < w.u.b0 + w.u.nb)
+              a.blk[((size_t)w.r * a.table_stride + b + blk) * d.Hq + w.h * d.G + r] = __log2f(y[i]) + step[r].ref;
           }
-          wait_st();
         }
-        uint8_t* p = sp + (tid >> 4) * (N * 16) + (tid & 15);
+        // the previous product is done with the probabilities' buffer
+        if (count > 0) ok = mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
+        umma::fence_after();
+        if constexpr (C::NO == 1) add_last(t);             // the next product takes its place
+        uint8_t* p = sp + (tid >> 4) * (NP * 16) + (tid & 15);
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
-          const uint32_t hi = float2_to_e4m3x2(x[r], x[r + 1]);
-          const float2 back = e4m3x2_to_float2(hi);
-          const uint32_t lo = float2_to_e4m3x2((x[r] - back.x) * kLoP, (x[r + 1] - back.y) * kLoP);
-          p[r * 16] = (uint8_t)hi;
-          p[(r + 1) * 16] = (uint8_t)(hi >> 8);
-          p[(r + RT) * 16] = (uint8_t)lo;
-          p[(r + RT + 1) * 16] = (uint8_t)(lo >> 8);
+          float f = x[r], g = x[r + 1];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const uint32_t code = float2_to_e5m2x2(f, g);
+            p[(r + i * RT) * 16] = (uint8_t)code;
+            p[(r + i * RT + 1) * 16] = (uint8_t)(code >> 8);
+            const float2 back = e5m2x2_to_float2(code);
+            f = (f - back.x) * kLoP;
+            g = (g - back.y) * kLoP;
+          }
         }
         umma::fence_async_smem();
         umma::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready));
+        if constexpr (C::NO > 1) add_last(t);              // under the next product
       }
       if (!ok) break;
       // the sums over the tokens; the next segment's queries while the last product runs
@@ -527,18 +581,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
       Walk x = w;
       x.next(a);
       if (x.left > 0) load_q(x, (seg + 1) & 1);
-      named_sync(1, 128);
       ok = mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
+      named_sync(1, 128);
       umma::fence_after();
       if (!ok) break;
-      float o[RT];
-      {
-        float s[N];
-#pragma unroll
-        for (int c = 0; c < N; c += 16) ld16(t_o + lanes + c, s + c);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) o[r] = fmaf(s[r + RT], 1.f / kLoP, s[r]);
-      }
+      add_product(count - 1, [](const RowStep&) { return 1.f; }, [](const RowStep& y) { return y.weight; });
 #pragma unroll
       for (int r = 0; r < RT; ++r) l[r] = ms.wsum[0][r] + ms.wsum[1][r] + ms.wsum[2][r] + ms.wsum[3][r];
       if (w.whole) {
@@ -548,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
           if (r < rows && tid < D)
             out[((size_t)(w.u.first + r / d.G) * d.Hq + w.h * d.G + r % d.G) * D + tid] =
                 __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
-          if (MASS && r < rows && tid == r) a.lse[(size_t)w.r * d.Hq + w.h * d.G + r] = m[r] + log2f(l[r]);
+          if (MASS && r < rows && tid == r) a.lse[(size_t)w.r * d.Hq + w.h * d.G + r] = most + log2f(l[r]);
         }
       } else {
         const size_t rec = (size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * RT;
@@ -556,14 +603,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
         for (int r = 0; r < RT; ++r)
           if (r < rows) {
             if (tid < D) a.part_o[(rec + r) * D + tid] = o[r];
-            if (tid == r) a.part_ml[rec + r] = make_float2(m[r], l[r]);
+            if (tid == r) a.part_ml[rec + r] = make_float2(most, l[r]);
           }
       }
       umma::fence_before();
       ++seg;
       w = x;
     }
-    if (!ok && lane == 0) paged_error(d, kErrTimeout);
+    if (!ok) paged_error(d, kErrTimeout);
   }
   __syncwarp();
   __syncthreads();

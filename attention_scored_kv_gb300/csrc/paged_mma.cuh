@@ -1,5 +1,5 @@
 // Helpers of the paged cache's tensor-core kernels: mbarriers with bounded waits, bulk
-// copies, unswizzled K-major operand descriptors, the E4M3 matrix instruction and TMEM
+// copies, unswizzled K-major operand descriptors, the 8-bit matrix instruction and TMEM
 // loads and stores beyond umma.cuh's.
 #pragma once
 #include "paged.cuh"
@@ -65,13 +65,14 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t k_step) {
   return ((saddr & 0x3FFFFu) >> 4) | ((k_step >> 4) << 16);
 }
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t row_step) { return (row_step >> 4) | (1u << 14); }
-// kind::f8f6f4, E4M3 operands, float32 accumulator.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// kind::f8f6f4, operands of either type, float32 accumulator.
+enum F8 : uint32_t { kE4M3 = 0, kE5M2 = 1 };
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, F8 a = kE4M3, F8 b = kE4M3) {
+  return (1u << 4) | (a << 7) | (b << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// D[tmem] (+)= A[smem] B[smem]^T, E4M3, where `on` is not 0.
-__device__ __forceinline__ void mma_e4m3(uint32_t on, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
-                                         uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[smem] B[smem]^T, 8-bit operands, where `on` is not 0.
+__device__ __forceinline__ void mma_f8(uint32_t on, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                       uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
       " setp.ne.b32 p, %7, 0;\n setp.ne.b32 q, %0, 0;\n"

@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
   } else if (warp == kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
     // ---- matrix instructions
-    constexpr uint32_t id_qk = idesc_e4m3(128, 128), id_pv = umma::idesc_f16(true, 128, D);
+    constexpr uint32_t id_qk = idesc_f8(128, 128), id_pv = umma::idesc_f16(true, 128, D);
     const uint32_t on = elect();
     int count = 0, count_b = 0;
     bool ok = true;
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       const uint32_t bk = desc_lo(smem_u32(sk + (n % kKStages) * C::K), 128);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)                    // the pieces hi, then lo, over the same K
-        mma_e4m3(on, tmem + x * 128, aq + k * (2 * kRows), desc_hi(128), bk + (k % (D / 32)) * 16, desc_hi(8 * D),
+        mma_f8(on, tmem + x * 128, aq + k * (2 * kRows), desc_hi(128), bk + (k % (D / 32)) * 16, desc_hi(8 * D),
                  id_qk, k > 0);
       commit(on, smem_u32(&ms.s_ready[x]));
     };

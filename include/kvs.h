@@ -620,11 +620,14 @@ KVS_API kvs_status kvs_paged_gather(kvs_paged* pc, int32_t layer, int32_t n_rows
  * that the row sees a part of; other entries are left as they were.
  * d_scratch: device memory of kvs_paged_attend_scratch_bytes(), 256-byte aligned, whose
  * contents before and after mean nothing; calls that may overlap need scratch of their
- * own.  With bf16 in_dtype probabilities are rounded to 8 significant bits or more before
- * their product with V; sums and softmax statistics are float32.  On the tensor cores V's
- * scale rides in the probability's exponent: where a page's V scale is 2^-100 of that of a
- * row's heaviest token (a page of zeros, 2^-100, beside values of 224 to 448), weights under
- * 2^-26 of the heaviest are taken as 0, and a bit sooner for every factor of 2 more. */
+ * own.  Sums and softmax statistics are float32.  With bf16 in_dtype a probability is rounded
+ * before its product with V: with at most 16 query rows to a request and KV head (32 with block
+ * masses) to 11 significant bits, down to 2^-29 of the heaviest of its 128 neighbours and by
+ * no more than 2^-38 of that below; with more rows to bf16.  KVS_KERNEL_GENERAL keeps
+ * float32 throughout.  On the tensor cores V's scale rides in the probability's exponent:
+ * where a page's V scale is 2^-100 of that of a row's heaviest token (a page of zeros, 2^-100,
+ * beside values of 224 to 448), weights under 2^-26 of the heaviest are taken as 0, and a
+ * bit sooner for every factor of 2 more. */
 KVS_API size_t kvs_paged_attend_scratch_bytes(const kvs_paged* pc, int32_t n_reqs, int32_t table_stride,
                                               int32_t total_q, int32_t max_q_len, int32_t block_mass);
 KVS_API kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const int32_t* d_block_table,
