@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           if (lane == (r & 31)) ms.wmax[count & 1][warp][r] = top;
         }
-        named_sync(1, 128);
+        ok = named_and(1, 128, ok);                        // the same in all threads: none is left waiting here
         if (!ok) break;
         if (lane < RT) {
           const auto& wm = ms.wmax[count & 1];
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
       x.next(a);
       if (x.left > 0) load_q(x, (seg + 1) & 1);
       ok = mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
-      named_sync(1, 128);
+      ok = named_and(1, 128, ok);
       umma::fence_after();
       if (!ok) break;
       add_product(count - 1, [](const RowStep&) { return 1.f; }, [](const RowStep& y) { return y.weight; });

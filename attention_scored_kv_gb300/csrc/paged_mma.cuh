@@ -49,6 +49,15 @@ __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("barrier.sync %0, %1;" :: "r"(id), "r"(n) : "memory");
 }
 
+// As named_sync, and whether `mine` holds in all of its threads: the same answer in each.
+__device__ __forceinline__ bool named_and(int id, int n, bool mine) {
+  __syncwarp();
+  uint32_t all;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.and.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(all) : "r"((uint32_t)mine), "r"(id), "r"(n) : "memory");
+  return all != 0;
+}
+
 // Matrix instructions are issued by a whole warp in step, with one lane predicated on: the
 // operands then stay in uniform registers.  A single lane in a branch of its own took 80 to
 // 160 clocks an instruction to set them up, more than the 64 that 128 x 128 x 32 bytes takes.
