@@ -68,8 +68,11 @@ def _load_call():
 class PagedCache:
     """A kvs_paged context bound to a workspace this object owns (a torch uint8 tensor).
 
-    Work goes on `stream`, by default the current stream of the cache's device.  Outputs
-    that a method allocates are safe to use on that stream.
+    Work goes on `stream`, by default the current stream of the cache's device.  What a
+    method allocates is allocated on that stream, so that no earlier work of another stream
+    still uses the memory, and may be used on it and, once that waits for it, on the current
+    one.  The workspace outlives the work that any stream has with it; a graph that was
+    captured over a cache needs the cache to live as long.
 
     plan, append, gather and attend on the current stream, with outputs of their own, are
     taken by an extension module; it declines what it does not find in order, and the
@@ -88,8 +91,10 @@ class PagedCache:
         self.device, self._index, self._lib = device, device.index, lib()
         nbytes = paged_workspace_bytes(cfg)
         self._ctx = ctypes.c_void_p()
+        self._streams = set()                # raw handles of the streams that have used the workspace
         with torch.cuda.device(device):
-            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            with torch.cuda.stream(stream):  # None: the current one
+                self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
             st = self._lib.kvs_paged_create(ctypes.byref(cfg), self.workspace.data_ptr(), nbytes, self._stream(stream),
                                             ctypes.byref(self._ctx))
         if st != _abi.OK:
@@ -113,7 +118,20 @@ class PagedCache:
             raise KVSError(st, self.last_error())
 
     def _stream(self, stream):
-        return _raw_stream(self._index) if stream is None else stream.cuda_stream
+        if stream is None:
+            raw = _raw_stream(self._index)
+        else:
+            if stream.device != self.device:
+                raise ValueError("stream must be on %s, got one on %s" % (self.device, stream.device))
+            raw = stream.cuda_stream
+        if raw not in self._streams:
+            self._mark(raw, stream)
+        return raw
+
+    def _mark(self, raw, stream=None):
+        """The workspace's memory is not reused before this stream is done with it."""
+        self.workspace.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+        self._streams.add(raw)
 
     # A call of a decode step runs on the GPU for a few microseconds, so the checks are spelled out for the
     # tensors that pass and leave the message to _need.
@@ -134,9 +152,13 @@ class PagedCache:
         return shape
 
     def _empty(self, shape, dtype, stream):
-        t = _empty(shape, dtype=dtype, device=self.device)
-        if stream is not None:
-            t.record_stream(stream)      # freed memory is not reused before the launch has run
+        if stream is None:
+            return _empty(shape, dtype=dtype, device=self.device)
+        if stream.device != self.device:
+            raise ValueError("stream must be on %s, got one on %s" % (self.device, stream.device))
+        with torch.cuda.stream(stream):
+            t = _empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))      # where the caller is likely to read it
         return t
 
     # ---- tables
@@ -147,6 +169,8 @@ class PagedCache:
         [capacity] whose size is free_count [1].  free_count_out (default: free_count)
         and kv_len_out (may be ctx_len) receive the updated state.  Returns a PagedPlan."""
         if stream is None and kv_len_out is None and self._fast is not None:
+            if _raw_stream(self._index) not in self._streams:
+                self._mark(_raw_stream(self._index))
             r = self._fast.plan(self._key, ctx_len, new_len, block_table, free_pages, free_count,
                                 free_count if free_count_out is None else free_count_out, row_capacity)
             if r.__class__ is tuple:
@@ -210,6 +234,8 @@ class PagedCache:
     def append(self, layer, k, v, slots, stream=None):
         """Store k, v [rows, Hkv, D] (input dtype) at slots [rows]."""
         if stream is None and self._fast is not None:
+            if _raw_stream(self._index) not in self._streams:
+                self._mark(_raw_stream(self._index))
             st = self._fast.append(self._key, layer, k, v, slots)
             if st == 0:
                 return
@@ -226,6 +252,8 @@ class PagedCache:
     def gather(self, layer, slots, k_out=None, v_out=None, stream=None):
         """The values at slots [rows]: (k, v), each [rows, Hkv, D] in the input dtype."""
         if stream is None and k_out is None and v_out is None and self._fast is not None:
+            if _raw_stream(self._index) not in self._streams:
+                self._mark(_raw_stream(self._index))
             r = self._fast.gather(self._key, layer, slots)
             if r.__class__ is tuple:
                 return r
@@ -257,6 +285,8 @@ class PagedCache:
         block_mass: optional float32 [n, stride] that receives each visible block's mass
         (single-token rows only).  scratch: optional uint8 tensor of attend_scratch_bytes."""
         if stream is None and out is None and scratch is None and self._fast is not None:
+            if _raw_stream(self._index) not in self._streams:
+                self._mark(_raw_stream(self._index))
             r = self._fast.attend(self._key, layer, q, block_table, kv_len, q_start, max_q_len, window, block_mass)
             if r.__class__ is _Tensor:
                 return r
