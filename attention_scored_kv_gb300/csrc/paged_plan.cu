@@ -115,9 +115,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
       if (TAKE) a.kv_len[r] = grant ? c + q : c;
     }
     if (TAKE) {
-      // table entries, a thread to a page
-      const int pages = s_page[m];
-      for (int j = s_page[0] + cta * kThreads + tid; j < pages; j += G * kThreads) {
+      // Table entries, a thread to a page.  Pages that are wanted past the stack's are of denied requests; together
+      // they may pass 32 bits.
+      const int pages = min(s_page[m], count);
+      for (long long j0 = (long long)s_page[0] + cta * kThreads + tid; j0 < pages; j0 += (long long)G * kThreads) {
+        const int j = (int)j0;
         int i = 0, top = m - 1;
         while (i < top) {
           const int mid = (i + top + 1) >> 1;
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
     }
     // rows, four to a thread
     const int lo = s_start[0], hi = min(s_start[m], a.capacity);
-    for (int t0 = (lo & ~3) + 4 * (cta * kThreads + tid); t0 < hi; t0 += 4 * G * kThreads) {
+    for (int t0 = lo < hi ? (lo & ~3) + 4 * (cta * kThreads + tid) : hi; t0 < hi; t0 += 4 * G * kThreads) {
       int i = 0, top = m - 1;                // the last request that starts at or before the first row
       const int key = max(t0, lo);
       while (i < top) {
