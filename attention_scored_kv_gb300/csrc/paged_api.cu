@@ -7,6 +7,7 @@
 #include <string>
 
 #include "paged.cuh"
+#include "paged_cut.h"
 #include "trace.cuh"
 
 using namespace kvs;
@@ -156,6 +157,14 @@ PagedAttendPlan plan_attend(const kvs_paged* pc, int n_reqs, int stride, int tot
   return p;
 }
 
+// Whether a CTA's share of the work stays within 32 bits.
+bool work_fits(const kvs_paged* pc, int n_reqs, int stride, int total_q, int max_q_len, bool mass) {
+  const PagedAttendPlan p = plan_attend(pc, n_reqs, stride, total_q, max_q_len, mass);
+  const long long per = paged_prompt_rows() / pc->dev.G;
+  return p.kernel == PagedAttendPlan::kGeneral ||
+         cut::share_fits(p.kernel == PagedAttendPlan::kDecode ? n_reqs : total_q / per + n_reqs, stride, pc->dev.Hkv, p.grid);
+}
+
 kvs_status check_attend(kvs_paged* pc, int32_t n_reqs, int32_t table_stride, int32_t total_q, int32_t max_q_len,
                         bool mass) {
   if (n_reqs < 1 || n_reqs > kMaxReqs)
@@ -167,6 +176,9 @@ kvs_status check_attend(kvs_paged* pc, int32_t n_reqs, int32_t table_stride, int
                 max_q_len);
   if (mass && max_q_len != 1)
     return fail(pc, KVS_ERR_UNSUPPORTED, "block masses need single-token queries (max_q_len 1, got %d)", max_q_len);
+  if (!work_fits(pc, n_reqs, table_stride, total_q, max_q_len, mass))
+    return fail(pc, KVS_ERR_UNSUPPORTED, "%d rows over tables of %d blocks are too much for one call: split the rows", total_q,
+                table_stride);
   return KVS_OK;
 }
 
@@ -326,7 +338,8 @@ size_t kvs_paged_attend_scratch_bytes(const kvs_paged* pc, int32_t n_reqs, int32
                                       int32_t max_q_len, int32_t block_mass) {
   Trace trace_("kvs_paged_attend_scratch_bytes");
   if (!pc || n_reqs < 1 || n_reqs > kMaxReqs || table_stride < 1 || table_stride > kMaxStride || total_q < 0 || total_q > (1 << 28) ||
-      max_q_len < 1 || (block_mass && max_q_len != 1))
+      max_q_len < 1 || (block_mass && max_q_len != 1) ||
+      !work_fits(pc, n_reqs, table_stride, total_q, max_q_len, block_mass != 0))
     return 0;
   const size_t n = plan_attend(pc, n_reqs, table_stride, total_q, max_q_len, block_mass != 0).total;
   return n ? n : 256;

@@ -35,6 +35,7 @@
 // 89 us (5.95 TB/s, 89 % of the measured copy rate), 64 of 1024 to 32768 with masses 187 us;
 // one of 131072 on 64/8 heads 52 us (5.2 TB/s), where about 4 us before the first copy
 // and the join weigh more; one of 700 tokens 10 us, the call included.
+#include "paged_cut.h"
 #include "paged_mma.cuh"
 
 namespace kvs {
@@ -42,8 +43,8 @@ namespace {
 
 using namespace pmma;
 
-constexpr int kTile = 128;               // tokens of a tile
-constexpr int kTileBlocks = kTile / kBlock;
+using cut::kTileBlocks;
+constexpr int kTile = kTileBlocks * kBlock;      // tokens of a tile
 constexpr int kThreads = 192;            // 4 softmax warps, copies, matrix instructions
 constexpr int kCtasPerSm = 2;
 constexpr float kLog2e = 1.4426950408889634f;

@@ -36,6 +36,7 @@
 // the other tile's overlaps: 2950 clocks a step of 128 tokens, against 2048 of matrix work, 61 % of the
 // tensor core's time.  Measured on 32/4 heads of 128: an 8192-token prompt 437 us (1.26 PFLOP/s,
 // 66 % of the measured bf16 rate), five chunks of 100 to 2048 tokens behind up to 8192 314 us (1.20 PFLOP/s).
+#include "paged_cut.h"
 #include "paged_mma.cuh"
 
 namespace kvs {
@@ -43,14 +44,17 @@ namespace {
 
 using namespace pmma;
 
-constexpr int kTile = 128, kTileBlocks = kTile / kBlock;
+using cut::kSetup;
+using cut::kTileBlocks;
+using cut::Unit;
+constexpr int kTile = kTileBlocks * kBlock;
+static_assert(kTile == 128 && kBlock == cut::kTokens, "tiles");
 constexpr int kThreads = 512;            // 8 softmax warps, K copies, matrix, query copies, a spare, 4 V warps
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kQWarp = 10, kVWarp = 12, kVThreads = 128;
 // Registers of a softmax thread and of the others: 256 (168 + 88) = the block's 65536.
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 constexpr int kKStages = 3, kVStages = 2, kQStages = 1;
 constexpr int kSlots = 4;                // scales of this many tiles, row factors of this many segments
-constexpr int kSetup = 3;                // what a unit's start costs, in tiles, where work is cut
 constexpr int kRows = 128;               // rows of a tile of queries
 constexpr int kChunk = 512;              // requests of one round of the search
 constexpr float kLog2e = 1.4426950408889634f;
@@ -76,35 +80,21 @@ __device__ __forceinline__ Req req_of(const PagedAttend& a, int r) {
   x.p0 = min(max(__ldg(a.kv_len + r), 0), a.table_stride * kBlock) - n;
   return x;
 }
-struct Unit {
-  int i0, cnt;           // first query token of the request, tokens
-  int b0, nb, tiles;     // blocks that any of them sees
-  __device__ int cost() const { return tiles + kSetup; }
-};
 __device__ __forceinline__ Unit unit_of(const PagedAttend& a, const Req& x, int qg, int per) {
-  Unit u;
-  u.i0 = qg * per;
-  u.cnt = min(per, x.n - u.i0);
-  const int hi = max(x.p0 + u.i0 + u.cnt, 0);
-  const int lo = a.window > 0 ? max(x.p0 + u.i0 + 1 - a.window, 0) : 0;
-  u.b0 = lo / kBlock;
-  u.nb = max((hi + kBlock - 1) / kBlock - u.b0, 0);
-  u.tiles = max((u.nb + kTileBlocks - 1) / kTileBlocks, 1);
-  return u;
+  return cut::unit_of(x.p0, x.n, a.window, qg, per);
 }
 
 struct Search {
   long long sums[32];
   long long total, before;
-  int tiles[kChunk];
+  long long tiles[kChunk];
   int r, qg, h, t;
 };
 
 // Cost of request r per KV head, by a warp: tiles and units' starts.
-__device__ int request_tiles(const PagedAttend& a, int r, int per) {
+__device__ long long request_tiles(const PagedAttend& a, int r, int per) {
   const Req x = req_of(a, r);
-  int sum = 0;
-  for (int qg = threadIdx.x & 31; qg * per < x.n; qg += 32) sum += unit_of(a, x, qg, per).cost();
+  long long sum = cut::lane_cost(x.p0, x.n, a.window, per, threadIdx.x & 31, 32);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
@@ -115,7 +105,7 @@ __device__ long long total_tiles(const PagedAttend& a, int per, int warps, Searc
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long sum = 0;
   for (int r = warp; r < a.n_reqs; r += warps) {
-    const int t = request_tiles(a, r, per);
+    const long long t = request_tiles(a, r, per);
     if (lane == 0 && r < kChunk) s.tiles[r] = t;
     sum += t;
   }
@@ -136,7 +126,7 @@ __device__ void locate(const PagedAttend& a, int per, int warps, long long targe
     if (r0 > 0) {
       __syncthreads();
       for (int i = warp; i < m; i += warps) {
-        const int t = request_tiles(a, r0 + i, per);
+        const long long t = request_tiles(a, r0 + i, per);
         if (lane == 0) s.tiles[i] = t;
       }
     }
@@ -145,7 +135,7 @@ __device__ void locate(const PagedAttend& a, int per, int warps, long long targe
     if (warp == 0) {
       long long at = base;
       for (int i = 0; i < m; i += 32) {
-        const long long mine = i + lane < m ? (long long)s.tiles[i + lane] * hkv : 0;
+        const long long mine = i + lane < m ? s.tiles[i + lane] * hkv : 0;
         long long upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

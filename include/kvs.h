@@ -611,6 +611,8 @@ KVS_API kvs_status kvs_paged_gather(kvs_paged* pc, int32_t layer, int32_t n_rows
  * h / (Hq / Hkv).  A row that sees nothing gets zeros; one whose query is not finite
  * gets NaN.  Rows past row_start[n_reqs] are left
  * as they were.  d_row_start NULL: one row per request (total_q must be n_reqs).
+ * A call whose rows and tables are so large that an SM's share of it passes 2^31 tiles of 128
+ * tokens is refused (KVS_ERR_UNSUPPORTED).
  * max_q_len: at least the most rows any request has (1 when d_row_start is NULL); rows past
  * it, or past total_q, are left as they were and reported as KVS_ERR_CAPACITY.  kv_len is
  * clamped to [0, table_stride * 16].

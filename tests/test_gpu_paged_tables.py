@@ -33,3 +33,14 @@ def test_plan_that_wants_more_pages_than_32_bits_count(alias):
     assert cpu(p.positions).tolist() == list(range(16)) + list(range(cap - 16))
     assert cpu(p.row_start)[[0, 1, 2]].tolist() == [0, 16, 16 + (1 << 26)]
     assert cache.get_status() == _abi.ERR_CAPACITY
+
+
+def test_calls_with_more_work_than_a_cta_counts_are_refused():
+    """By the sizes alone, before any array is looked at."""
+    cache = make(hq=64, hkv=8, d=128, pages=2)
+    lib = kvs.lib()
+    for n, stride, rows, most in ((1 << 20, 1 << 22, 1 << 20, 1), (1, 1 << 22, 1 << 28, 1 << 28)):
+        assert lib.kvs_paged_attend_scratch_bytes(cache._ctx, n, stride, rows, most, 0) == 0
+        st = lib.kvs_paged_attend(cache._ctx, 0, n, None, stride, None, 256, rows, most, 0, *[None] * 4, 0, None)
+        assert st == _abi.ERR_UNSUPPORTED and "too much for one call" in cache.last_error()
+    assert lib.kvs_paged_attend_scratch_bytes(cache._ctx, 1024, 8192, 1024, 1, 0) > 0
