@@ -24,6 +24,7 @@ constexpr int kScaleMinExp = -100;       // exponents a page scale can have
 constexpr int kScaleMaxExp = 119;
 constexpr float kFloatMax = 3.402823466e38f;
 constexpr int kMaxGroup = 64;            // query heads per KV head at most
+constexpr int kMaxTableStride = 1 << 22; // blocks of a request: positions and tile counts fit 32 bits
 
 struct PagedDev {
   int32_t L, Hq, Hkv, G, D, num_pages, in_dtype;

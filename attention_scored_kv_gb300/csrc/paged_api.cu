@@ -22,7 +22,7 @@ struct kvs_paged {
 
 namespace {
 
-constexpr int32_t kMaxStride = 1 << 22, kMaxReqs = 1 << 20;   // of block tables: positions and tile counts fit 32 bits
+constexpr int32_t kMaxStride = kMaxTableStride, kMaxReqs = 1 << 20;   // of block tables
 
 void put(char* msg, size_t n, const char* fmt, ...) {
   if (!msg || n == 0) return;

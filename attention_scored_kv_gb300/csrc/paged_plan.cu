@@ -206,51 +206,68 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
   if (err) paged_error(a.d, err);
 }
 
-// One CTA: the number of pages first, then each page to its place on the stack.
+// One CTA walks the pages from the last to the first, so that a page's place on the stack is the number of
+// those after it that are pages: what is not one is left out without knowing the total first.  A thread has four
+// pages in a row, whose table entries are loaded together.
+constexpr int kReleaseChunk = 256;       // requests of one round: their pages are counted in 32 bits
+static_assert((long long)kReleaseChunk * kMaxTableStride <= 1ll << 30, "pages of a round");
 __global__ void __launch_bounds__(kThreads) release_kernel(const PagedDev d, int n, const int32_t* kv_len,
                                                            int32_t* table, int stride, int32_t* free_pages,
                                                            int free_capacity, int32_t* free_count) {
   __shared__ Item warp_sums[kThreads / 32];
-  __shared__ int s_first[kChunk + 1];
+  __shared__ int s_first[kReleaseChunk + 1];
   const int tid = threadIdx.x;
-  const int count = max(0, min(*free_count, free_capacity));
-  auto blocks_of = [&](int r) {
-    return r < n ? (int)min((max((long long)kv_len[r], 0ll) + kBlock - 1) / kBlock, (long long)stride) : 0;
-  };
-  long long total = 0;
-  for (int r0 = 0; r0 < n; r0 += kChunk) {
-    block_scan(Item{0, blocks_of(r0 + tid)}, warp_sums);
-    total += warp_sums[kThreads / 32 - 1].pages;
-    __syncthreads();
-  }
+  long long count = max(0, min(*free_count, free_capacity));
   int err = 0;
-  long long carry = 0;
-  for (int r0 = 0; r0 < n; r0 += kChunk) {
-    const int m = min(kChunk, n - r0), mine = blocks_of(r0 + tid);
+  for (int r0 = (n - 1) / kReleaseChunk * kReleaseChunk; r0 >= 0; r0 -= kReleaseChunk) {
+    const int m = min(kReleaseChunk, n - r0);
+    const int mine = tid < m ? (int)min((max((long long)kv_len[r0 + tid], 0ll) + kBlock - 1) / kBlock, (long long)stride) : 0;
     const Item incl = block_scan(Item{0, mine}, warp_sums);
     if (tid < m) s_first[tid] = (int)(incl.pages - mine);
     const int here = (int)warp_sums[kThreads / 32 - 1].pages;
     if (tid == 0) s_first[m] = here;
     __syncthreads();
-    for (int j = tid; j < here; j += kThreads) {
-      int i = 0, top = m - 1;
-      while (i < top) {
-        const int mid = (i + top + 1) >> 1;
-        if (s_first[mid] <= j) i = mid; else top = mid - 1;
+    for (int top = here; top > 0; top -= 4 * kThreads) {       // pages [top - 2048, top), the last four first
+      int page[4], good = 0;
+      const int j0 = top - 1 - 4 * tid;
+      int i = 0, last = m - 1;
+      while (i < last) {
+        const int mid = (i + last + 1) >> 1;
+        if (s_first[mid] <= max(j0, 0)) i = mid; else last = mid - 1;
       }
-      int32_t* entry = table + (size_t)(r0 + i) * stride + (j - s_first[i]);
-      const int page = *entry;
-      *entry = -1;
-      const long long at = count + total - 1 - (carry + j);
-      const bool bad = page < 0 || page >= d.num_pages;
-      if (bad) err |= kErrState;
-      if (at >= free_capacity) err |= kErrCapacity;
-      else free_pages[at] = bad ? -1 : page;
+      int32_t* entry[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 - u;
+        while (j >= 0 && j < s_first[i]) --i;
+        entry[u] = j >= 0 ? table + (size_t)(r0 + i) * stride + (j - s_first[i]) : nullptr;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) page[u] = entry[u] ? *entry[u] : -1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (!entry[u]) continue;
+        *entry[u] = -1;
+        if (page[u] >= 0 && page[u] < d.num_pages) {
+          ++good;
+        } else {
+          page[u] = -1;
+          err |= kErrState;
+        }
+      }
+      long long at = count + block_scan(Item{0, good}, warp_sums).pages - good;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (page[u] < 0) continue;
+        if (at < free_capacity) free_pages[at] = page[u];
+        else err |= kErrCapacity;
+        ++at;
+      }
+      count += warp_sums[kThreads / 32 - 1].pages;
+      __syncthreads();
     }
-    carry += here;
-    __syncthreads();
   }
-  if (tid == 0) *free_count = (int)min((long long)count + total, (long long)free_capacity);
+  if (tid == 0) *free_count = (int)min(count, (long long)free_capacity);
   if (err) paged_error(d, err);
 }
 

@@ -576,7 +576,7 @@ KVS_API kvs_status kvs_paged_slot_map(kvs_paged* pc, int32_t n_reqs, const int32
  * stack and set their table entries to -1.  The stack is left as if the pages had never
  * been taken by a kvs_paged_plan that took them in this order.  Pages that do not fit in
  * free_capacity are dropped (KVS_ERR_CAPACITY by kvs_paged_get_status), entries that are
- * not a page are skipped over as a dropped -1 (KVS_ERR_STATE).  A page shared by several
+ * not a page are left out (KVS_ERR_STATE).  A page shared by several
  * requests must be released once only.  d_free_count: [1] in/out.  One launch. */
 KVS_API kvs_status kvs_paged_release(kvs_paged* pc, int32_t n_reqs, const int32_t* d_kv_len, int32_t* d_block_table,
                                      int32_t table_stride, int32_t* d_free_pages, int32_t free_capacity,

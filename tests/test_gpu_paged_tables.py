@@ -44,3 +44,46 @@ def test_calls_with_more_work_than_a_cta_counts_are_refused():
         st = lib.kvs_paged_attend(cache._ctx, 0, n, None, stride, None, 256, rows, most, 0, *[None] * 4, 0, None)
         assert st == _abi.ERR_UNSUPPORTED and "too much for one call" in cache.last_error()
     assert lib.kvs_paged_attend_scratch_bytes(cache._ctx, 1024, 8192, 1024, 1, 0) > 0
+
+
+def released(kv, table, stack, count, num_pages):
+    """kvs_paged_release in plain Python: (stack, count, table)."""
+    stack, table, order = list(stack), np.array(table), []
+    for r, x in enumerate(kv):
+        for b in range(min(-(-max(int(x), 0) // 16), table.shape[1])):
+            if 0 <= table[r, b] < num_pages:
+                order.append(table[r, b])
+            table[r, b] = -1
+    for page in reversed(order):
+        if count < len(stack):
+            stack[count] = page
+            count += 1
+    return stack, count, table
+
+
+@pytest.mark.parametrize("n,stride,room", [(1, 1, 0), (1, 1, 9), (3, 40, 0), (5, 3000, 100), (256, 9, 3), (257, 40, 0), (900, 30, -500)])
+@pytest.mark.parametrize("bad", [0.0, 0.2, 1.0])
+def test_release_leaves_out_what_is_not_a_page(n, stride, room, bad):
+    """A later plan gets pages only; their order is the reverse of the one that they were taken in."""
+    rng = np.random.default_rng(n + stride)
+    kv = rng.integers(-3, stride * 16 + 40, n)
+    blocks = np.minimum(-(-np.maximum(kv, 0) // 16), stride)
+    pages = int(blocks.sum()) + 3
+    table = np.full((n, stride), -9)
+    perm, at = rng.permutation(pages), 0
+    for r, b in enumerate(blocks):
+        table[r, :b] = perm[at:at + b]
+        at += b
+    spoilt = (rng.random((n, stride)) < bad) & (np.arange(stride)[None] < blocks[:, None])
+    table[spoilt] = rng.choice([-1, pages, 2 ** 31 - 1, -2 ** 31], int(spoilt.sum()))
+    stack = np.concatenate([perm[at:], np.full(max(pages - 3 + room, 0), -7)])
+    cache = make(hq=1, hkv=1, d=16, pages=pages)
+    t, s, c = i32(table), i32(stack), i32([3])
+    cache.release(i32(kv), t, s, c)
+    want_s, want_c, want_t = released(kv, table, stack, 3, pages)
+    assert cpu(c)[0] == want_c and cpu(s).tolist() == list(want_s) and np.array_equal(cpu(t), want_t)
+    got = cpu(s)[:want_c]
+    assert ((got >= 0) & (got < pages)).all() and len(set(got.tolist())) == want_c
+    full = len(blocks) and int((table[np.arange(stride)[None] < blocks[:, None]] >= 0).sum()) > len(stack) - 3
+    st = cache.get_status()
+    assert st in ((_abi.ERR_STATE, _abi.ERR_CAPACITY) if spoilt.any() or full else (0,))
