@@ -717,7 +717,8 @@ cudaError_t launch_d(const PagedAttend& a, int rows, int grid, cudaStream_t st) 
   switch (rows) {
     case 8: return mass ? launch<D, 8, true>(a, grid, st) : launch<D, 8, false>(a, grid, st);
     case 16: return mass ? launch<D, 16, true>(a, grid, st) : launch<D, 16, false>(a, grid, st);
-    default: return launch<D, 32, true>(a, grid, st);      // masses of 17 to 32 heads a group
+    case 32: return mass ? launch<D, 32, true>(a, grid, st) : cudaErrorInvalidValue;      // 17 to 32 heads a group
+    default: return cudaErrorInvalidValue;
   }
 }
 
@@ -725,8 +726,9 @@ cudaError_t launch_d(const PagedAttend& a, int rows, int grid, cudaStream_t st) 
 
 int paged_decode_ctas_per_sm() { return kCtasPerSm; }
 
-// rows: 8, 16 or 32, at least max_q_len * G.
+// rows: 8, 16 or (with block masses) 32, at least max_q_len * G.
 cudaError_t launch_paged_decode(const PagedAttend& a, int rows, int grid, cudaStream_t st) {
+  if ((long long)a.max_q_len * a.d.G > rows || (a.mass && (!a.blk || !a.lse))) return cudaErrorInvalidValue;
   return a.d.D == 64 ? launch_d<64>(a, rows, grid, st) : launch_d<128>(a, rows, grid, st);
 }
 
