@@ -103,10 +103,12 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     at::Tensor k = fresh(c, {n, c.hkv, c.d}, c.dtype), v = fresh(c, {n, c.hkv, c.d}, c.dtype);
     const kvs_status st = g_gather(c.pc, (int32_t)layer, (int32_t)n, i32(slots), k.data_ptr(), v.data_ptr(), stream_of(c));
     if (st != KVS_OK) return PyLong_FromLong(st);
-    PyObject* r = PyTuple_New(2);
-    if (!r) return nullptr;
-    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(k)));
-    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(v)));
+    PyObject* both[2] = {THPVariable_Wrap(std::move(k)), THPVariable_Wrap(std::move(v))};
+    PyObject* r = both[0] && both[1] ? PyTuple_New(2) : nullptr;
+    for (int i = 0; i < 2; ++i) {
+      if (r) PyTuple_SET_ITEM(r, i, both[i]);
+      else Py_XDECREF(both[i]);
+    }
     return r;
   });
 }
@@ -125,21 +127,36 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     TAKE(add->numel() == n && table->size(0) == n && count->numel() == 1 && out->numel() == 1);
     const long rows = PyLong_AsLong(a[7]);
     TAKE(rows >= 0 && rows <= (1 << 30) && n <= (1 << 20) && stride <= INT32_MAX && pages->numel() <= INT32_MAX);
-    // one allocation, slots and positions on 16-byte boundaries
+    // one allocation, slots and positions on 16-byte boundaries; all that may fail comes before the call, which takes
+    // pages: the method must not make it again
     const int64_t pos = rows + (-rows & 3), start = pos + rows, len = start + n + 1, den = len + n;
     at::Tensor buf = fresh(c, {den + 1}, at::kInt);
+    PyObject* r = PyTuple_New(5);
+    if (!r) return nullptr;
+    {
+      at::AutoDispatchBelowADInplaceOrView below;   // whole numbers: nothing to differentiate
+      const int64_t part[5][2] = {{start, n + 1}, {len, n}, {0, rows}, {pos, rows}, {den, 1}};
+      try {
+        for (int i = 0; i < 5; ++i) {
+          PyObject* view = THPVariable_Wrap(buf.as_strided({part[i][1]}, {1}, part[i][0]));
+          if (!view) {
+            Py_DECREF(r);
+            return nullptr;
+          }
+          PyTuple_SET_ITEM(r, i, view);
+        }
+      } catch (...) {
+        Py_DECREF(r);
+        throw;
+      }
+    }
     int32_t* p = i32(&buf);
     const kvs_status st = g_plan(c.pc, (int32_t)n, i32(ctx), i32(add), i32(table), (int32_t)stride, i32(pages),
                                  (int32_t)pages->numel(), i32(count), i32(out), p + start, p + len, p, p + pos,
                                  (int32_t)rows, p + den, stream_of(c));
-    if (st != KVS_OK) return PyLong_FromLong(st);
-    at::AutoDispatchBelowADInplaceOrView below;     // whole numbers: nothing to differentiate
-    PyObject* r = PyTuple_New(5);
-    if (!r) return nullptr;
-    const int64_t part[5][2] = {{start, n + 1}, {len, n}, {0, rows}, {pos, rows}, {den, 1}};
-    for (int i = 0; i < 5; ++i)
-      PyTuple_SET_ITEM(r, i, THPVariable_Wrap(buf.as_strided({part[i][1]}, {1}, part[i][0])));
-    return r;
+    if (st == KVS_OK) return r;
+    Py_DECREF(r);
+    return PyLong_FromLong(st);
   });
 }
 

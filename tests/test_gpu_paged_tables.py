@@ -87,3 +87,26 @@ def test_release_leaves_out_what_is_not_a_page(n, stride, room, bad):
     full = len(blocks) and int((table[np.arange(stride)[None] < blocks[:, None]] >= 0).sum()) > len(stack) - 3
     st = cache.get_status()
     assert st in ((_abi.ERR_STATE, _abi.ERR_CAPACITY) if spoilt.any() or full else (0,))
+
+
+def test_a_plan_whose_outputs_fail_takes_its_pages_once():
+    """The extension's views fail (as under a dispatch mode that refuses them): the method makes the call, once."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class NoStrided(TorchDispatchMode):
+        seen = 0
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            if "as_strided" in str(func):
+                NoStrided.seen += 1
+                raise RuntimeError("refused")
+            return func(*args, **(kwargs or {}))
+
+    cache = make(pages=20)
+    table = torch.full((2, 8), -1, dtype=torch.int32, device="cuda")
+    ctx, new, free, count = i32([0, 0]), i32([20, 5]), i32(np.arange(20)), i32([20])
+    with NoStrided():
+        p = cache.plan(ctx, new, table, free, count, 25)
+    assert NoStrided.seen == 1
+    assert cpu(count)[0] == 17 and cpu(table)[:, :2].tolist() == [[19, 18], [17, -1]]
+    assert cpu(p.slots)[:3].tolist() == [304, 305, 306] and cpu(p.kv_len).tolist() == [20, 5]
