@@ -1,6 +1,7 @@
 """ctypes declarations of libkvs (include/kvs.h).  Argument marshalling only."""
 
 import ctypes
+import operator
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -60,8 +61,25 @@ class PagedConfig(ctypes.Structure):
                 ("in_dtype", ctypes.c_int32), ("kernel", ctypes.c_int32), ("reserved", ctypes.c_int32 * 8)]
 
 
+def int32(x):
+    """x as an int of 32 bits: ctypes cuts a larger one to its low bits without a word."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError("%d does not fit 32 bits" % x)
+    return x
+
+
+class _Int32:
+    """A checked 32-bit argument (ctypes raises an ArgumentError with the ValueError's text)."""
+
+    @classmethod
+    def from_param(cls, x):
+        return ctypes.c_int32(int32(x))
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_N = _Int32
 _S = Seqs
 _SIGS = {
     "kvs_config_init": (None, [ctypes.POINTER(Config)]),
@@ -97,13 +115,13 @@ _SIGS = {
     "kvs_paged_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PagedConfig)]),
     "kvs_paged_create": (_I, [ctypes.POINTER(PagedConfig), _P, ctypes.c_size_t, _P, ctypes.POINTER(_P)]),
     "kvs_paged_destroy": (_I, [_P]),
-    "kvs_paged_plan": (_I, [_P, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
-    "kvs_paged_slot_map": (_I, [_P, _I, _P, _P, _P, _I, _P, _P, _P, _I, _P]),
-    "kvs_paged_release": (_I, [_P, _I, _P, _P, _I, _P, _I, _P, _P]),
-    "kvs_paged_append": (_I, [_P, _I, _I, _P, _P, _P, _P]),
-    "kvs_paged_gather": (_I, [_P, _I, _I, _P, _P, _P, _P]),
-    "kvs_paged_attend_scratch_bytes": (ctypes.c_size_t, [_P, _I, _I, _I, _I, _I]),
-    "kvs_paged_attend": (_I, [_P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kvs_paged_plan": (_I, [_P, _N, _P, _P, _P, _N, _P, _N, _P, _P, _P, _P, _P, _P, _N, _P, _P]),
+    "kvs_paged_slot_map": (_I, [_P, _N, _P, _P, _P, _N, _P, _P, _P, _N, _P]),
+    "kvs_paged_release": (_I, [_P, _N, _P, _P, _N, _P, _N, _P, _P]),
+    "kvs_paged_append": (_I, [_P, _N, _N, _P, _P, _P, _P]),
+    "kvs_paged_gather": (_I, [_P, _N, _N, _P, _P, _P, _P]),
+    "kvs_paged_attend_scratch_bytes": (ctypes.c_size_t, [_P, _N, _N, _N, _N, _N]),
+    "kvs_paged_attend": (_I, [_P, _N, _N, _P, _N, _P, _P, _N, _N, _N, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "kvs_paged_get_status": (_I, [_P, _P]),
     "kvs_paged_clear_error": (_I, [_P, _P]),
     "kvs_paged_last_error": (ctypes.c_char_p, [_P]),

@@ -31,7 +31,7 @@ def paged_config_init(**fields):
     cfg = _abi.PagedConfig()
     lib().kvs_paged_config_init(ctypes.byref(cfg))
     for k, v in fields.items():
-        setattr(cfg, k, v)
+        setattr(cfg, k, _abi.int32(v) if isinstance(getattr(cfg, k, None), int) else v)
     return cfg
 
 
