@@ -17,7 +17,8 @@ from . import _abi, KVSError, _need, _TORCH_DT, lib
 
 _Tensor, _i32, _f32 = torch.Tensor, torch.int32, torch.float32
 _empty = torch.empty
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# absent where torch is built without CUDA: the host-side calls work there too
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 PagedPlan = collections.namedtuple("PagedPlan", "row_start kv_len slots positions denied")
 PagedPlan.__doc__ = """What one plan made: row_start [n + 1], kv_len [n], slots and positions
