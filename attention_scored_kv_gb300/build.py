@@ -70,11 +70,21 @@ def _link(objs, lib):
 
 
 def _build_call():
-    """The binding's extension module."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """The binding's extension module.  The library and the binding work without it, so what it needs
+    beyond them (g++, torch's and Python's headers) may be missing: that is said, and None returned."""
+    spec = importlib.util.find_spec("torch")
+    torch = os.path.dirname(spec.origin) if spec and spec.origin else ""
+    needs = {"g++": shutil.which("g++"),
+             "torch's headers": os.path.exists(os.path.join(torch, "include", "ATen", "ATen.h")),
+             "torch with CUDA": os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")),
+             "Python's headers": os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))}
+    missing = [k for k, v in needs.items() if not v]
+    if missing:
+        print("paged_call.cpp is not built (no %s): paged calls go through ctypes" % ", ".join(missing), file=sys.stderr)
+        return None
     newest = max(os.path.getmtime(CALL_SRC), os.path.getmtime(os.path.join(INCLUDE, "kvs.h")))
     if os.path.exists(CALL) and os.path.getmtime(CALL) >= newest:
-        return
+        return CALL
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     dirs = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
             sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
@@ -86,6 +96,7 @@ def _build_call():
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s\n%s" % (CALL_SRC, " ".join(cmd), r.stderr))
+    return CALL
 
 
 def build(verbose=False, ptxas_info=False, debug=True):

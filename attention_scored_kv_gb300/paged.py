@@ -10,6 +10,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -51,15 +52,21 @@ _call = None
 
 
 def _load_call():
-    """The extension that makes the calls of a decode step (csrc/paged_call.cpp), bound to the loaded library."""
+    """The extension that makes the calls of a decode step (csrc/paged_call.cpp), bound to the loaded library.
+    None where it was not built, or not for this torch: every call then goes through ctypes."""
     global _call
     if _call is None:
         path = os.path.join(os.path.dirname(_abi.LIB_PATH), "_paged_call.so")
         if not os.path.exists(path):
-            raise RuntimeError("_paged_call.so is not built (%s); run python -m attention_scored_kv_gb300.build" % path)
+            warnings.warn("_paged_call.so is not built (%s): paged calls take 5 to 20 us longer each" % path)
+            return None
         loader = importlib.machinery.ExtensionFileLoader("_paged_call", path)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_paged_call", loader))
-        loader.exec_module(module)
+        try:
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_paged_call", loader))
+            loader.exec_module(module)
+        except ImportError as e:
+            warnings.warn("_paged_call.so does not load (%s): paged calls take 5 to 20 us longer each" % e)
+            return None
         module.bind(*(ctypes.cast(getattr(lib(), "kvs_paged_" + f), ctypes.c_void_p).value
                       for f in ("plan", "append", "gather", "attend", "attend_scratch_bytes")))
         _call = module
@@ -76,8 +83,8 @@ class PagedCache:
     captured over a cache needs the cache to live as long.
 
     plan, append, gather and attend on the current stream, with outputs of their own, are
-    taken by an extension module; it declines what it does not find in order, and the
-    method's own checks say why."""
+    taken by an extension module, where it is built; it declines what it does not find in
+    order, and the method's own checks say why."""
 
     _fast = None
 
