@@ -108,6 +108,11 @@ __device__ __forceinline__ uint32_t float2_to_e5m2x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(__half2 v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&v)));
+  return r;
+}
 __device__ __forceinline__ float2 e5m2x2_to_float2(uint32_t codes16) {
   const uint32_t h = __byte_perm(codes16, 0, 0x1404);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));

@@ -13,7 +13,7 @@
 //
 // Precision: E4M3 holds 4 significant bits.  A bf16 query (8 bits) is split in two pieces
 // of 4, hi = rn(q), lo = rn(16 (q - hi)) after a power of two brings the row's largest to
-// (224, 448]: exact for elements within 2^14 of it, off by 2^-22 of it at most below.  A
+// (224, 448]: exact for elements within 2^13 of it, off by 2^-21 of it at most below.  A
 // probability is three E5M2 pieces, each of 8 times the remainder of the one before: off by
 // at most 2^-11 of itself down to 2^-29 of the tile's heaviest and by 2^-38 of the heaviest
 // below that.  The range is what matters: a head whose sink takes nearly all the weight has a

@@ -3,8 +3,8 @@
 //
 // A unit is a (request, KV head) and up to 256 query rows (tokens x heads of the group, two
 // tiles A and B of 128), which share every K and V they read.  Per 128 cached tokens:
-//   S = Q K^T        two pieces of Q (4 significant bits each) as one contraction of 2 D,
-//                    E4M3 x E4M3, K as it is stored
+//   S = Q K^T        two pieces of Q (E4M3, the remainder E5M2) as one contraction of 2 D,
+//                    K as it is stored (E4M3)
 //   t = S kscale c_r + log2 vscale,  m_r: the t of some token that the row has seen
 //   x = 2^(t - m_r) rounded to bf16,  l_r += x / vscale,  O += X V      bf16 x bf16
 // and o = O / l.  The scales are powers of two, so V's rides in x's exponent and V's codes
@@ -14,7 +14,9 @@
 // float32's exponents, so m need not follow the maximum: it moves, and O is rescaled, only where x would pass
 // 2^63 or l leave float32.  With x in f16, whose 2^16 strong tokens passed in four of ten tiles of
 // the 8192-token prompt, the exponentials taken again and O rescaled cost it a fifth.
-// Queries: exact down to 2^-10 of the row's largest element, an error of 2^-19 of the largest below that.
+// Queries: a bf16 element has 8 significant bits, its first piece 4, and the remainder then at most 3, which E5M2
+// holds down to steps of 2^-16: exact down to 2^-13 of the row's largest element, off by 2^-21 of the largest at most
+// below that.  (With E4M3 for both pieces, whose steps end at 2^-9, it was 2^-10 and 2^-17.)
 //
 // How: work is cut as in the decode kernel: the 128-token tiles of all units laid end to
 // end and split evenly over one CTA per SM, partials of split units added by a join
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(kRows) split_kernel(const PagedAttend a, const
       const float2 f = unpack2(mul2(pack2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u)), up));
       const __half2 v = __floats2half2_rn(f.x, f.y);
       const uint32_t c1 = f16x2_to_e4m3x2(v);
-      const uint32_t c2 = f16x2_to_e4m3x2(__hsub2(v, e4m3x2_to_half2(c1)));
+      const uint32_t c2 = f16x2_to_e5m2x2(__hsub2(v, e4m3x2_to_half2(c1)));
       hi4[u / 2] = u & 1 ? hi4[u / 2] | c1 << 16 : c1;
       lo4[u / 2] = u & 1 ? lo4[u / 2] | c2 << 16 : c2;
     }
@@ -635,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
   } else if (warp == kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
     // ---- matrix instructions
-    constexpr uint32_t id_qk = idesc_f8(128, 128), id_pv = umma::idesc_f16(true, 128, D);
+    constexpr uint32_t id_hi = idesc_f8(128, 128), id_lo = idesc_f8(128, 128, kE5M2), id_pv = umma::idesc_f16(true, 128, D);
     const uint32_t on = elect();
     int count = 0, count_b = 0;
     bool ok = true;
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)                    // the pieces hi, then lo, over the same K
         mma_f8(on, tmem + x * 128, aq + k * (2 * kRows), desc_hi(128), bk + (k % (D / 32)) * 16, desc_hi(8 * D),
-                 id_qk, k > 0);
+                 k < D / 32 ? id_hi : id_lo, k > 0);
       commit(on, smem_u32(&ms.s_ready[x]));
     };
     auto products = [&](int x, int n, uint32_t parity, bool first, bool last) {    // O, and the next S, of tile x

@@ -625,8 +625,9 @@ KVS_API kvs_status kvs_paged_gather(kvs_paged* pc, int32_t layer, int32_t n_rows
  * own.  Sums and softmax statistics are float32.  With bf16 in_dtype a probability is rounded
  * before its product with V: with at most 16 query rows to a request and KV head (32 with block
  * masses) to 11 significant bits, down to 2^-29 of the heaviest of its 128 neighbours and by
- * no more than 2^-38 of that below; with more rows to bf16.  KVS_KERNEL_GENERAL keeps
- * float32 throughout.  On the tensor cores V's scale rides in the probability's exponent:
+ * no more than 2^-38 of that below; with more rows to bf16.  A query's elements are exact
+ * down to 2^-13 of the largest of their head, and off by no more than 2^-21 of it below.
+ * KVS_KERNEL_GENERAL keeps float32 throughout.  On the tensor cores V's scale rides in the probability's exponent:
  * where a page's V scale is 2^-100 of that of a row's heaviest token (a page of zeros, 2^-100,
  * beside values of 224 to 448), weights under 2^-26 of the heaviest are taken as 0, and a
  * bit sooner for every factor of 2 more. */
