@@ -66,6 +66,7 @@ __host__ __device__ inline size_t k_code(int D, int t, int d) {
 }
 
 __device__ __forceinline__ void paged_error(const PagedDev& d, int32_t bits) { atomicOr(d.err, bits); }
+__device__ __forceinline__ void set_error(const PagedDev& d, int32_t bits) { paged_error(d, bits); }   // KVS_DCHECK's
 
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }

@@ -390,6 +390,10 @@ kvs_status kvs_paged_attend(kvs_paged* pc, int32_t layer, int32_t n_reqs, const 
   a.q_factors = reinterpret_cast<float*>(s + p.q_factors);
   a.cuts = reinterpret_cast<int32_t*>(s + p.cuts);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+#ifdef KVS_DEBUG
+  // what the kernels read of the scratch they have written: partials start as NaN, cuts as -1
+  if (cudaMemsetAsync(d_scratch, 0xFF, p.total, cs) != cudaSuccess) return cuda_ok(pc, cudaGetLastError(), "attend");
+#endif
   cudaError_t e = p.kernel == PagedAttendPlan::kDecode   ? launch_paged_decode(a, p.rows, p.grid, cs)
                   : p.kernel == PagedAttendPlan::kPrompt ? launch_paged_prompt(a, p.grid, cs)
                                                          : launch_paged_general(a, cs);

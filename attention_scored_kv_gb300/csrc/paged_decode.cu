@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
 #pragma unroll
           for (int i = 0; i < EACH; ++i) {
             const int r = row * EACH + i;
-            if ((RT >= 16 || !(lane & 1)) && r < rows && b + blk < w.u.b0 + w.u.nb)
+            if ((RT >= 16 || !(lane & 1)) && r < rows && b + blk < w.u.b0 + w.u.nb &&
+                KVS_DCHECK(d, w.r < a.n_reqs && b >= 0 && b + blk < a.table_stride && w.h * d.G + r < d.Hq))
               a.blk[((size_t)w.r * a.table_stride + b + blk) * d.Hq + w.h * d.G + r] = __log2f(y[i]) + step[r].ref;
           }
         }
@@ -589,7 +590,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
       add_product(count - 1, [](const RowStep&) { return 1.f; }, [](const RowStep& y) { return y.weight; });
 #pragma unroll
       for (int r = 0; r < RT; ++r) l[r] = ms.wsum[0][r] + ms.wsum[1][r] + ms.wsum[2][r] + ms.wsum[3][r];
-      if (w.whole) {
+      if (!KVS_DCHECK(d, w.u.first >= 0 && w.u.first + w.u.n <= a.total_q && w.h < d.Hkv)) {
+      } else if (w.whole) {
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -633,7 +635,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttend a)
   const int4 cut = *reinterpret_cast<const int4*>(a.cuts + (blockIdx.x + 1) * 8);
   const int r = cut.x, h = cut.y, c0 = blockIdx.x, n = cut.z - c0 + 1;
   if (cut.z == 0) return;
+  if (!KVS_DCHECK(d, r >= 0 && r < a.n_reqs && h >= 0 && h < d.Hkv && cut.z > c0 && cut.z <= (int)gridDim.x && cut.w >> 1 == 0)) return;
   const Unit u = unit_of(a, r);
+  if (!KVS_DCHECK(d, u.first >= 0 && u.n > 0 && u.first + u.n <= a.total_q)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kJoinRows, group = warp / kJoinRows;
   const int row = blockIdx.y * kJoinRows + mine;
   const bool live = row < u.n * d.G;

@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kWarps * 32) general_kernel(const PagedAttend 
             a.blk[((size_t)x.r * a.table_stride + b) * d.Hq + head * d.G + g0 + g] = -INFINITY;
         continue;
       }
+      if (!KVS_DCHECK(d, x.r < a.n_reqs && b >= 0 && b < a.table_stride)) continue;
       const size_t at = (size_t)page * d.Hkv + head;
       const float2 sc = d.scales[a.layer * d.layer_scales + at];
       const uint8_t* kb = d.k + a.layer * d.layer_bytes + at * (16 * D);

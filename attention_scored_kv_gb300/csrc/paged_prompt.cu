@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kRows) split_kernel(const PagedAttend a, const
   }
   const Req q = req_of(a, lo);
   const int i0 = (id - query_tile(q.first, lo, qpt)) * qpt;
-  if (i0 < 0 || i0 >= q.n) return;
+  if (i0 < 0 || i0 >= q.n || !KVS_DCHECK(d, q.first >= 0 && q.first + q.n <= a.total_q)) return;
   const int i = i0 + row / d.G;
   const bool live = row / d.G < qpt && i < q.n;
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
@@ -554,7 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       if (lane == 0) mbar_expect(full, tiles * (C::Q + kRows * 4));
       __syncwarp();
       if (lane < tiles) {
-        const size_t at = (size_t)(query_tile(w.q.first + w.u.i0 + lane * qpt, w.r, qpt)) * d.Hkv + w.h;
+        int id = query_tile(w.q.first + w.u.i0 + lane * qpt, w.r, qpt);
+        if (!KVS_DCHECK(d, id >= 0 && id < a.total_q / qpt + a.n_reqs && w.h < d.Hkv)) id = 0;
+        const size_t at = (size_t)id * d.Hkv + w.h;
         bulk_load(smem_u32(sq + (buf * 2 + lane) * C::Q), a.q_pieces + at * C::Q, C::Q, full);
         bulk_load(smem_u32(&ms.qc[slot][lane * kRows]), a.q_factors + at * kRows, kRows * 4, full);
       }
@@ -785,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PagedAttend a
       ok = warp_wait(smem_u32(&ms.o_done[x]), seg & 1);
       if (!ok) break;
       umma::fence_after();
-      const bool live = token < qpt && i < w.u.cnt;
+      const bool live = token < qpt && i < w.u.cnt && KVS_DCHECK(d, w.q.first >= 0 && w.q.first + w.u.i0 + i < a.total_q);
       if (w.whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
@@ -841,7 +843,9 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const PagedAt
   const int* at = a.cuts + (blockIdx.x + 1) * 8;
   const int c0 = blockIdx.x, c1 = at[3], r = at[0], qg = at[1], h = at[2], slot = at[4];
   if (c1 == 0) return;
+  if (!KVS_DCHECK(d, r >= 0 && r < a.n_reqs && h >= 0 && h < d.Hkv && c1 > c0 && c1 <= (int)gridDim.x && slot >> 1 == 0)) return;
   const Req q = req_of(a, r);
+  if (!KVS_DCHECK(d, qg >= 0 && qg * 2 * qpt < q.n && q.first >= 0 && q.first + q.n <= a.total_q)) return;
   const Unit u = unit_of(a, q, qg, 2 * qpt);
   __shared__ float weight[kMostParts][kJoinRows + 1], total[kJoinRows];
   const int n = c1 - c0 + 1;

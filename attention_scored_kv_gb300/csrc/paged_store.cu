@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const PagedDev d, i
     for (int j = 0; j < 16; ++j) {
       const int off = __shfl_sync(0xffffffffu, s, j) & 15;
       if (j < len) {
-        if (lane == off) run.row = i + j;
+        if (lane == off && KVS_DCHECK(d, i + j < n_rows)) run.row = i + j;
         run.have |= 1u << off;
       }
     }
