@@ -424,9 +424,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
       *reinterpret_cast<int4*>(a.cuts + blockIdx.x * 8) = make_int4(w.r, w.h, last, off > before);
     }
     named_sync(1, 128);                                    // qc of all rows
+    // `ok`: this thread's waits; `go`: all threads' up to the last barrier, by which they leave the loops alike (none
+    // is left waiting at a barrier)
     int count = 0, seg = 0;
-    bool ok = true;
-    while (w.left > 0 && ok) {
+    bool ok = true, go = true;
+    while (w.left > 0) {
       float l[RT], o[RT];                                  // of the thread's token and of its dimension
 #pragma unroll
       for (int r = 0; r < RT; ++r) l[r] = o[r] = 0.f;
@@ -499,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           if (lane == (r & 31)) ms.wmax[count & 1][warp][r] = top;
         }
-        ok = named_and(1, 128, ok);                        // the same in all threads: none is left waiting here
-        if (!ok) break;
+        go = named_and(1, 128, ok);
+        if (!go) break;
         if (lane < RT) {
           const auto& wm = ms.wmax[count & 1];
           const float top = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
           }
         }
         // the previous product is done with the probabilities' buffer
-        if (count > 0) ok = mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
+        if (count > 0) ok = ok && mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
         umma::fence_after();
         if constexpr (C::NO == 1) add_last(t);             // the next product takes its place
         uint8_t* p = sp + (tid >> 4) * (NP * 16) + (tid & 15);
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
         if (lane == 0) mbar_arrive(smem_u32(&ms.p_ready));
         if constexpr (C::NO > 1) add_last(t);              // under the next product
       }
-      if (!ok) break;
+      if (!go) break;
       // the sums over the tokens; the next segment's queries while the last product runs
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
@@ -583,10 +585,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
       Walk x = w;
       x.next(a);
       if (x.left > 0) load_q(x, (seg + 1) & 1);
-      ok = mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
-      ok = named_and(1, 128, ok);
+      ok = ok && mbar_wait(smem_u32(&ms.o_done), (count - 1) & 1);
+      go = named_and(1, 128, ok);
       umma::fence_after();
-      if (!ok) break;
+      if (!go) break;
       add_product(count - 1, [](const RowStep&) { return 1.f; }, [](const RowStep& y) { return y.weight; });
 #pragma unroll
       for (int r = 0; r < RT; ++r) l[r] = ms.wsum[0][r] + ms.wsum[1][r] + ms.wsum[2][r] + ms.wsum[3][r];
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Page
       ++seg;
       w = x;
     }
-    if (!ok) paged_error(d, kErrTimeout);
+    if (!go) paged_error(d, kErrTimeout);
   }
   __syncwarp();
   __syncthreads();
