@@ -32,8 +32,8 @@
 // product up to 16 rows: the last one is added while the next is computed.
 //
 // Bound by the pages' bytes.  Measured on 32/4 heads of 128: 16 contexts of 32768 tokens
-// 89 us (5.95 TB/s, 89 % of the measured copy rate), 64 of 1024 to 32768 with masses 187 us;
-// one of 131072 on 64/8 heads 52 us (5.2 TB/s), where about 4 us before the first copy
+// 89 us (5.95 TB/s, 89 % of the measured copy rate), 64 of 1024 to 32768 with masses 190 us;
+// one of 131072 on 64/8 heads 53 us (5.1 TB/s), where about 4 us before the first copy
 // and the join weigh more; one of 700 tokens 10 us, the call included.
 #include "paged_cut.h"
 #include "paged_mma.cuh"

@@ -289,7 +289,8 @@ class PagedCache:
         """Attend q [rows, Hq, D] (input dtype) over the pages; returns out of q's shape and
         type.  Without q_start there is one row per request; with it (int32 [n + 1], a
         plan's row_start) request r's rows are q_start[r] .. q_start[r + 1] - 1, its last
-        tokens, at most max_q_len of them.  window > 0: only the last `window` positions.
+        tokens, at most max_q_len of them; rows behind the last request's are not written
+        (a padded batch's are whatever was in memory).  window > 0: only the last `window` positions.
         block_mass: optional float32 [n, stride] that receives each visible block's mass
         (single-token rows only).  scratch: optional uint8 tensor of attend_scratch_bytes."""
         if stream is None and out is None and scratch is None and self._fast is not None:

@@ -619,7 +619,8 @@ KVS_API kvs_status kvs_paged_gather(kvs_paged* pc, int32_t layer, int32_t n_rows
  * d_block_mass_opt (max_q_len 1 only): [n_reqs][table_stride] float32; entry b of request r
  * receives the maximum over query heads of the head's weight in block b ("Per-Head
  * Attention as a Scoring Signal", Fix: score per head, place per block), for the blocks
- * that the row sees a part of; other entries are left as they were.
+ * that the row sees a part of; other entries are left as they were.  A head whose query is not
+ * finite has no part in it.
  * d_scratch: device memory of kvs_paged_attend_scratch_bytes(), 256-byte aligned, whose
  * contents before and after mean nothing; calls that may overlap need scratch of their
  * own.  Sums and softmax statistics are float32.  With bf16 in_dtype a probability is rounded

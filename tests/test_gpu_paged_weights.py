@@ -17,6 +17,7 @@ Tolerance per output element, all from the exact weights a_j in 64 bits, with A 
   last piece, which is 2^-38 of the tile's heaviest a_j * (V scale): T = sum over tiles of
   max_j(a_j * V scale) sum_j |V code|.
 """
+import functools
 import math
 
 import numpy as np
@@ -77,6 +78,13 @@ def check(out, want, d, dt, r, smallest):
     assert (err <= tol).all(), ((err / tol).max(), (err / np.abs(o)).max())
 
 
+@functools.lru_cache(maxsize=1)
+def sink_oracle(ctx, weight, sigma, d):
+    k, v, q = sink_case(ctx, weight, sigma, 64, d, 40, seed=d)
+    _, orc, table = stored([ctx], k, v, d, 64, 1, 7)
+    return k, v, q, orc, table
+
+
 SINKS = [(100, 0.99, 1.0), (128, 0.9999, 1.0), (1000, 0.9999, 1.0), (5000, 0.999, 2.0), (32768, 0.99, 1.0),
          (32768, 0.999, 1.0), (131072, 0.99, 0.5), (131072, 0.9999, 0.5), (131072, 0.99, 2.0)]
 
@@ -88,8 +96,11 @@ SINKS = [(100, 0.99, 1.0), (128, 0.9999, 1.0), (1000, 0.9999, 1.0), (5000, 0.999
 def test_sinks_without_value(ctx, weight, sigma, d, hq, rows):
     if rows == 40 and ctx > 5000:
         rows = 20
-    k, v, q = sink_case(ctx, weight, sigma, hq, d, rows, seed=d + hq + rows)
-    cache, orc, table = stored([ctx], k, v, d, hq, 1, 7)
+    k, v, q, orc, table = sink_oracle(ctx, weight, sigma, d)
+    q = q[:rows, :hq].contiguous()
+    cache = kvs.PagedCache(kvs.paged_config_init(num_layers=1, num_q_heads=hq, num_kv_heads=1, head_dim=d,
+                                                 num_pages=orc.num_pages))
+    cache.append(0, k.cuda(), v.cuda(), i32(table[0, np.arange(ctx) // 16] * 16 + np.arange(ctx) % 16))
     want = exact(orc, table, ctx, q)
     out = cache.attend(0, q.cuda(), i32(table), i32([ctx]), q_start=i32([0, rows]), max_q_len=rows)
     if hq * rows <= 16:
@@ -131,3 +142,30 @@ def test_sinks_in_float32(rows):
     wide.append(0, k.float().cuda(), v.float().cuda(), slots)
     out = wide.attend(0, q.float().cuda(), i32(table), i32([ctx]), q_start=i32([0, rows]), max_q_len=rows)
     check(out, exact(orc, table, ctx, q), d, kvs.F32, 2.0 ** -23, 0.0)
+
+
+@pytest.mark.parametrize("hq,kernel", [(8, kvs.KERNEL_AUTO), (32, kvs.KERNEL_AUTO), (8, kvs.KERNEL_GENERAL)])
+def test_masses_leave_out_heads_that_are_not_finite(hq, kernel):
+    """The others' masses are as before; where no head is finite they are 0."""
+    ctx, d = 900, 128
+    g = torch.Generator().manual_seed(hq)
+    k, v = (torch.randn((2 * ctx, 1, d), generator=g).bfloat16() for _ in range(2))
+    q = torch.randn((2, hq, d), generator=g).bfloat16()
+    cache, orc, table = stored([ctx, ctx], k, v, d, hq, 1, 7)
+    if kernel == kvs.KERNEL_GENERAL:
+        cache = kvs.PagedCache(kvs.paged_config_init(num_layers=1, num_q_heads=hq, num_kv_heads=1, head_dim=d,
+                                                     num_pages=cache.cfg.num_pages, kernel=kernel))
+        slots = np.concatenate([table[r, np.arange(ctx) // 16] * 16 + np.arange(ctx) % 16 for r in range(2)])
+        cache.append(0, k.cuda(), v.cuda(), i32(slots))
+    bad = q.clone()
+    bad[0, 1, 5], bad[0, 4, 100] = float("nan"), float("-inf")
+    bad[1, :, 0] = float("inf")
+    mass = torch.full(table.shape, -3.0, device="cuda")
+    out = cache.attend(0, bad.cuda(), i32(table), i32([ctx, ctx]), block_mass=mass)
+    keep = [h for h in range(hq) if h not in (1, 4)]
+    want = orc.attend(f64(q[:1, keep]), table[:1], [ctx])
+    reach = want["reach"].max()
+    delta = (d + 8) * 2.0 ** -23 * reach + 2.0 ** -21 * (1 + reach)
+    assert (np.abs(f64(mass)[0] - want["mass"][0]) <= 8 * delta * want["mass"][0] + 1e-30).all()
+    assert (mass[1] == 0).all() and out[1].isnan().all() and out[0, 1].isnan().all()
+    assert out[0, keep].isfinite().all() and cache.get_status() == 0
